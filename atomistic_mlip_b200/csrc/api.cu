@@ -137,6 +137,26 @@ e2f_status cg_conv_impl(const void *x, int dtype, const float *pos, const e2f_cs
 e2f_status attention_backward_impl(const void *x, const float *pos, const e2f_csr *csr, const e2f_weights *w,
                                    const float *G, float *dx, float *dpos, cudaStream_t s);
 
+e2f_status embed_forward_impl(const void *ids, int id_type, int64_t N, const void *table, int dtype, int64_t V, int D,
+                              float scale, int Q, void *out, int out_dtype, cudaStream_t s);
+e2f_status embed_backward_impl(const void *ids, int id_type, int64_t N, const void *grad_out, int dtype, int64_t V, int D,
+                               float scale, int Q, float *grad_table, int accumulate, cudaStream_t s);
+
+static bool float_type(int32_t t) { return t == E2F_F32 || t == E2F_BF16; }
+static bool aligned_elem(const void *p, int32_t type) {
+  const uintptr_t b = type == E2F_BF16 ? 2 : type == E2F_I64 ? 8 : 4;
+  return reinterpret_cast<uintptr_t>(p) % b == 0;
+}
+
+static e2f_status validate_embed(int32_t id_type, int64_t N, int32_t dtype, int64_t V, int32_t D, float scale, int32_t Q) {
+  if (id_type != E2F_I32 && id_type != E2F_I64) return E2F_ERR_UNSUPPORTED;
+  if (!float_type(dtype)) return E2F_ERR_UNSUPPORTED;
+  if (N < 0 || N > INT32_MAX || V < 1 || V >= INT32_MAX || D < 1 || Q < 1) return E2F_ERR_INVALID_ARG;
+  if (D > (1 << 20) || (int64_t)Q * D > (1 << 30)) return E2F_ERR_UNSUPPORTED;
+  if (!(scale > -INFINITY && scale < INFINITY)) return E2F_ERR_INVALID_ARG;
+  return E2F_OK;
+}
+
 // q, k, v (library scratch), then the fused attention kernel; arguments
 // already validated.
 e2f_status attention_forward_impl(const void *x, const float *pos, const e2f_csr *csr, const e2f_weights *w,
@@ -301,6 +321,31 @@ e2f_status e2f_cg_conv_forward(const void *x, int32_t dtype, const float *pos, c
   if (!x || !pos || !W || !out) return E2F_ERR_INVALID_ARG;
   if (!aligned16(x) || !aligned16(out)) return E2F_ERR_INVALID_ARG;
   return cg_conv_impl(x, dtype, pos, csr, L, C, W, out, static_cast<cudaStream_t>(stream));
+}
+
+e2f_status e2f_embed_forward(const void *ids, int32_t id_type, int64_t N, const void *table, int32_t dtype, int64_t V,
+                             int32_t D, float scale, int32_t Q, void *out, int32_t out_dtype, void *stream) {
+  e2f_status st = validate_embed(id_type, N, dtype, V, D, scale, Q);
+  if (st != E2F_OK) return st;
+  if (!float_type(out_dtype)) return E2F_ERR_UNSUPPORTED;
+  if (N == 0) return E2F_OK;
+  if (!ids || !table || !out) return E2F_ERR_INVALID_ARG;
+  if (!aligned_elem(ids, id_type) || !aligned_elem(table, dtype) || !aligned_elem(out, out_dtype))
+    return E2F_ERR_INVALID_ARG;
+  return embed_forward_impl(ids, id_type, N, table, dtype, V, D, scale, Q, out, out_dtype,
+                            static_cast<cudaStream_t>(stream));
+}
+
+e2f_status e2f_embed_backward(const void *ids, int32_t id_type, int64_t N, const void *grad_out, int32_t dtype, int64_t V,
+                              int32_t D, float scale, int32_t Q, float *grad_table, int32_t accumulate, void *stream) {
+  e2f_status st = validate_embed(id_type, N, dtype, V, D, scale, Q);
+  if (st != E2F_OK) return st;
+  if (accumulate != 0 && accumulate != 1) return E2F_ERR_INVALID_ARG;
+  if (!grad_table || !aligned_elem(grad_table, E2F_F32)) return E2F_ERR_INVALID_ARG;
+  if (N > 0 && (!ids || !grad_out)) return E2F_ERR_INVALID_ARG;
+  if (!aligned_elem(ids, id_type) || !aligned_elem(grad_out, dtype)) return E2F_ERR_INVALID_ARG;
+  return embed_backward_impl(ids, id_type, N, grad_out, dtype, V, D, scale, Q, grad_table, accumulate,
+                             static_cast<cudaStream_t>(stream));
 }
 
 e2f_status e2f_stream_status(void *stream) {

@@ -18,7 +18,7 @@ import numpy as np
 
 _LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libe2f.so")
 MAX_L = 6
-F32, BF16 = 0, 1
+F32, BF16, I32, I64 = 0, 1, 2, 3
 
 STATUS = {0: "ok", 1: "invalid argument", 2: "cutoff too large", 3: "capacity",
           4: "unsupported", 5: "CUDA error", 6: "timeout", 7: "domain", 8: "scratch limit"}
@@ -77,6 +77,12 @@ SIGNATURES = {
     "e2f_cg_conv_forward": (ctypes.c_int32, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p, ctypes.POINTER(Csr),
                                              ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p, ctypes.c_void_p,
                                              ctypes.c_void_p]),
+    "e2f_embed_forward": (ctypes.c_int32, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p,
+                                           ctypes.c_int32, ctypes.c_int64, ctypes.c_int32, ctypes.c_float,
+                                           ctypes.c_int32, ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p]),
+    "e2f_embed_backward": (ctypes.c_int32, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p,
+                                            ctypes.c_int32, ctypes.c_int64, ctypes.c_int32, ctypes.c_float,
+                                            ctypes.c_int32, ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p]),
     "e2f_stream_status": (ctypes.c_int32, [ctypes.c_void_p]),
     "e2f_wigner_d": (ctypes.c_int32, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p,
                                       ctypes.c_void_p]),
@@ -357,6 +363,114 @@ def attention_backward(x, pos, nl: NeighborList, w: DeviceWeights, grad_out, str
                                         _ptr(grad_out), _ptr(gx), _ptr(gp), _stream_ptr(stream))
     _check(code, "e2f_attention_backward")
     return gx, gp
+
+
+# ----------------------------------------------------------------------------
+# the two ends of a model
+# ----------------------------------------------------------------------------
+_CODES = None
+
+
+def _code(t, what: str, kinds: str) -> int:
+    """Type code of a tensor for the C ABI; `kinds` 'f' (float32, bfloat16) or
+    'i' (int32, int64)."""
+    global _CODES
+    if _CODES is None:
+        torch = _torch()
+        _CODES = {"f": {torch.float32: F32, torch.bfloat16: BF16}, "i": {torch.int32: I32, torch.int64: I64}}
+    dt = t if not hasattr(t, "dtype") else t.dtype
+    code = _CODES[kinds].get(dt)
+    if code is None:
+        raise ValueError(f"{what} has type {dt}")
+    return code
+
+
+class _On:
+    """The device of a call's tensors and its stream: every tensor must be on
+    one CUDA device; the library works on the current one, so a call for
+    another device makes that the current one while it runs."""
+    __slots__ = ("stream", "_ctx")
+
+    def __init__(self, stream, **tensors):
+        torch = _torch()
+        dev = None
+        for name, t in tensors.items():
+            if t is None:
+                continue
+            if not t.is_cuda:
+                raise ValueError(f"{name} is not on a CUDA device")
+            if dev is None:
+                dev, first = t.device, name
+            elif t.device != dev:
+                raise ValueError(f"{name} is on {t.device}, {first} on {dev}")
+        self._ctx = None if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+        if stream is None:
+            stream = torch.cuda.current_stream(dev)
+        elif stream.device != dev:
+            raise ValueError(f"the stream is on {stream.device}, {first} on {dev}")
+        self.stream = stream.cuda_stream
+
+    def __enter__(self):
+        if self._ctx is not None:
+            self._ctx.__enter__()
+        return self.stream
+
+    def __exit__(self, *exc):
+        if self._ctx is not None:
+            self._ctx.__exit__(*exc)
+
+
+def _need(cond, msg: str):
+    if not cond:
+        raise ValueError(msg)
+
+
+def embed_forward(ids, table, scale: float = 1.0, Q: int = 1, out_dtype=None, out=None, stream=None):
+    """Features [N, Q, D] whose l = 0 row is scale * table[ids] and whose other
+    rows are zero (Q = 1: an embedding lookup).  ids int32 or int64 [N], -1 for
+    a padded row; table float32 or bfloat16 [V, D]; out_dtype float32 unless
+    given.  An id outside the table gives zeros and is reported by
+    stream_status()."""
+    torch = _torch()
+    _need(ids.dim() == 1 and ids.is_contiguous(), "ids must be a contiguous vector")
+    _need(table.dim() == 2 and table.is_contiguous(), "table must be contiguous [V, D]")
+    N, (V, D) = int(ids.shape[0]), table.shape
+    it, tt = _code(ids, "ids", "i"), _code(table, "table", "f")
+    if out is None:
+        out = torch.empty((N, Q, D), dtype=out_dtype or torch.float32, device=table.device)
+    else:
+        _need(out.shape == (N, Q, D) and out.is_contiguous(), f"out must be contiguous {(N, Q, D)}")
+        _need(out_dtype is None or out.dtype == out_dtype, "out has another type than out_dtype")
+    with _On(stream, ids=ids, table=table, out=out) as s:
+        code = lib().e2f_embed_forward(_ptr(ids), it, N, _ptr(table), tt, V, D, scale, Q, _ptr(out),
+                                       _code(out, "out", "f"), s)
+    _check(code, "e2f_embed_forward")
+    return out
+
+
+def embed_backward(ids, grad_out, V: int, scale: float = 1.0, grad_table=None, accumulate: bool = False, stream=None):
+    """Gradient float32 [V, D] of embed_forward's table: scale * the sum of the
+    l = 0 rows of grad_out (float32 or bfloat16 [N, Q, D] or [N, D]) over the
+    rows of each id.  With accumulate the sums are added to grad_table.  Sums
+    in a fixed order: the result repeats bit for bit."""
+    torch = _torch()
+    _need(ids.dim() == 1 and ids.is_contiguous(), "ids must be a contiguous vector")
+    _need(grad_out.dim() in (2, 3) and grad_out.is_contiguous(), "grad_out must be contiguous [N, Q, D] or [N, D]")
+    N, D = int(ids.shape[0]), int(grad_out.shape[-1])
+    _need(int(grad_out.shape[0]) == N, f"grad_out has {int(grad_out.shape[0])} rows, ids {N}")
+    Q = int(grad_out.shape[1]) if grad_out.dim() == 3 else 1
+    it, gt = _code(ids, "ids", "i"), _code(grad_out, "grad_out", "f")
+    if grad_table is None:
+        _need(not accumulate, "accumulate needs grad_table")
+        grad_table = torch.empty((V, D), dtype=torch.float32, device=grad_out.device)
+    else:
+        _need(grad_table.shape == (V, D) and grad_table.is_contiguous() and grad_table.dtype == torch.float32,
+              f"grad_table must be contiguous float32 {(V, D)}")
+    with _On(stream, ids=ids, grad_out=grad_out, grad_table=grad_table) as s:
+        code = lib().e2f_embed_backward(_ptr(ids), it, N, _ptr(grad_out), gt, V, D, scale, Q, _ptr(grad_table),
+                                        1 if accumulate else 0, s)
+    _check(code, "e2f_embed_backward")
+    return grad_table
 
 
 def project_qkv(x, w: DeviceWeights, stream=None):

@@ -58,11 +58,14 @@ typedef int32_t e2f_status;
 #define E2F_ERR_UNSUPPORTED      4  /* shape/dtype combination not implemented */
 #define E2F_ERR_CUDA             5  /* a CUDA runtime call failed (e2f_last_cuda_error) */
 #define E2F_ERR_TIMEOUT          6  /* a bounded device-side wait gave up */
-#define E2F_ERR_DOMAIN           7  /* a coordinate outside [0, box[k]) in a periodic dim */
+#define E2F_ERR_DOMAIN           7  /* a coordinate outside [0, box[k]) in a periodic dim;
+                                      an id outside the embedding table */
 #define E2F_ERR_SCRATCH_LIMIT    8  /* input larger than a fixed-scratch entry point allows */
 
 #define E2F_F32  0
 #define E2F_BF16 1
+#define E2F_I32  2   /* id types of the embedding calls */
+#define E2F_I64  3
 
 #define E2F_MAX_L 6
 
@@ -310,6 +313,54 @@ E2F_API int64_t e2f_cg_num_paths(int32_t L);
  */
 E2F_API e2f_status e2f_cg_conv_forward(const void *x, int32_t dtype, const float *pos, const e2f_csr *csr,
                                        int32_t L, int32_t C, const float *W, float *out, void *stream);
+
+/* ---------------------------------------------------------------------------
+ * The two ends of a model: ids -> node features, node features -> outputs.
+ * The node features the calls above read start from the species of the atoms
+ * ("E2Former-V2 ..." §4 and the summaries' energy heads name both ends but
+ * print no form for them); the plainest ones are taken.
+ * --------------------------------------------------------------------------*/
+
+/*
+ * e2f_embed_forward -- out[n][0][:] = scale * table[ids[n]], out[n][q][:] = 0
+ * for q > 0: the invariant (l = 0) features of every atom from its species,
+ * or, with Q = 1, a plain embedding lookup.
+ *
+ *   ids       device, [N] int32 or int64 (id_type E2F_I32 / E2F_I64), 0 <=
+ *             id < V.  -1 marks a padded row (zeros).  Any other value gives
+ *             a row of zeros too and latches E2F_ERR_DOMAIN for
+ *             e2f_stream_status.
+ *   table     device, [V][D] contiguous, `dtype` (E2F_F32 or E2F_BF16).
+ *   Q         rows per atom, >= 1 ((L+1)^2 for node features).
+ *   out       device, [N][Q][D] contiguous, `out_dtype`; fully overwritten.
+ *             The product is formed in fp32 and rounded once.
+ * Pointers need only their element's alignment (16 bytes and a width
+ * divisible by four or eight run fastest).  Fully asynchronous.
+ */
+E2F_API e2f_status e2f_embed_forward(const void *ids, int32_t id_type, int64_t N, const void *table, int32_t dtype,
+                                     int64_t V, int32_t D, float scale, int32_t Q, void *out, int32_t out_dtype,
+                                     void *stream);
+
+/*
+ * e2f_embed_backward -- grad_table[v][:] = scale * sum over the rows n with
+ * ids[n] = v of grad_out[n][0][:], the gradient of e2f_embed_forward.  With
+ * the structure index of every atom as its id it is also the per-structure
+ * sum of per-atom values.
+ *
+ *   ids         as above; rows with an id outside 0 .. V-1 take no part
+ *               (other than -1: E2F_ERR_DOMAIN is latched).
+ *   grad_out    device, [N][Q][D] contiguous, `dtype`; only the l = 0 row of
+ *               each atom is read.
+ *   grad_table  device fp32 [V][D] contiguous.  accumulate = 0: fully
+ *               overwritten (zeros for ids that do not occur); 1: the sums
+ *               are added to it.
+ * The rows are sorted by id (library scratch) and summed in fp32 in an order
+ * that depends on the ids alone: the result repeats bit for bit.  N <=
+ * 2^31 - 1.  Fully asynchronous.
+ */
+E2F_API e2f_status e2f_embed_backward(const void *ids, int32_t id_type, int64_t N, const void *grad_out, int32_t dtype,
+                                      int64_t V, int32_t D, float scale, int32_t Q, float *grad_table,
+                                      int32_t accumulate, void *stream);
 
 /*
  * e2f_stream_status -- synchronise `stream`, then return (and clear) any
