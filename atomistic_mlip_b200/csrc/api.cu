@@ -142,6 +142,11 @@ e2f_status embed_forward_impl(const void *ids, int id_type, int64_t N, const voi
 e2f_status embed_backward_impl(const void *ids, int id_type, int64_t N, const void *grad_out, int dtype, int64_t V, int D,
                                float scale, int Q, float *grad_table, int accumulate, cudaStream_t s);
 
+e2f_status linear_forward_impl(const e2f_linear *p, const void *residual, int64_t ldr, void *out, int64_t ldo,
+                               int out_dtype, cudaStream_t s);
+e2f_status linear_backward_impl(const e2f_linear *p, const void *grad_out, int64_t ldg, int out_dtype, void *grad_x,
+                                int64_t ldgx, void *grad_W, int64_t ldgw, float *grad_bias, cudaStream_t s);
+
 static bool float_type(int32_t t) { return t == E2F_F32 || t == E2F_BF16; }
 static bool aligned_elem(const void *p, int32_t type) {
   const uintptr_t b = type == E2F_BF16 ? 2 : type == E2F_I64 ? 8 : 4;
@@ -154,6 +159,22 @@ static e2f_status validate_embed(int32_t id_type, int64_t N, int32_t dtype, int6
   if (N < 0 || N > INT32_MAX || V < 1 || V >= INT32_MAX || D < 1 || Q < 1) return E2F_ERR_INVALID_ARG;
   if (D > (1 << 20) || (int64_t)Q * D > (1 << 30)) return E2F_ERR_UNSUPPORTED;
   if (!(scale > -INFINITY && scale < INFINITY)) return E2F_ERR_INVALID_ARG;
+  return E2F_OK;
+}
+
+// A row stride in elements: wide enough, and small enough that the byte offset of any row fits 62 bits.
+static bool stride_ok(int64_t ld, int32_t cols) { return ld >= cols && ld <= ((int64_t)1 << 29); }
+
+static e2f_status validate_linear(const e2f_linear *p, int32_t out_dtype) {
+  if (!p) return E2F_ERR_INVALID_ARG;
+  if (!float_type(p->dtype) || !float_type(out_dtype)) return E2F_ERR_UNSUPPORTED;
+  if (p->act != E2F_ACT_NONE && p->act != E2F_ACT_SILU && p->act != E2F_ACT_GELU) return E2F_ERR_UNSUPPORTED;
+  if (p->M < 0 || p->M > INT32_MAX || p->K < 1 || p->N < 1) return E2F_ERR_INVALID_ARG;
+  if (p->K > (1 << 20) || p->N > (1 << 20)) return E2F_ERR_UNSUPPORTED;
+  if (!stride_ok(p->ldx, p->K) || !stride_ok(p->ldw, p->K)) return E2F_ERR_INVALID_ARG;
+  if (p->M > 0 && (!p->x || !p->W)) return E2F_ERR_INVALID_ARG;
+  if (!aligned_elem(p->x, p->dtype) || !aligned_elem(p->W, p->dtype) || !aligned_elem(p->bias, E2F_F32))
+    return E2F_ERR_INVALID_ARG;
   return E2F_OK;
 }
 
@@ -346,6 +367,34 @@ e2f_status e2f_embed_backward(const void *ids, int32_t id_type, int64_t N, const
   if (!aligned_elem(ids, id_type) || !aligned_elem(grad_out, dtype)) return E2F_ERR_INVALID_ARG;
   return embed_backward_impl(ids, id_type, N, grad_out, dtype, V, D, scale, Q, grad_table, accumulate,
                              static_cast<cudaStream_t>(stream));
+}
+
+e2f_status e2f_linear_forward(const e2f_linear *p, const void *residual, int64_t ldr, void *out, int64_t ldo,
+                              int32_t out_dtype, void *stream) {
+  e2f_status st = validate_linear(p, out_dtype);
+  if (st != E2F_OK) return st;
+  if (!stride_ok(ldo, p->N) || (residual && !stride_ok(ldr, p->N))) return E2F_ERR_INVALID_ARG;
+  if (p->M == 0) return E2F_OK;
+  if (!out || out == p->x || out == p->W) return E2F_ERR_INVALID_ARG;
+  if (residual == out && ldr != ldo) return E2F_ERR_INVALID_ARG;
+  if (!aligned_elem(out, out_dtype) || !aligned_elem(residual, out_dtype)) return E2F_ERR_INVALID_ARG;
+  return linear_forward_impl(p, residual, ldr, out, ldo, out_dtype, static_cast<cudaStream_t>(stream));
+}
+
+e2f_status e2f_linear_backward(const e2f_linear *p, const void *grad_out, int64_t ldg, int32_t out_dtype, void *grad_x,
+                               int64_t ldgx, void *grad_W, int64_t ldgw, float *grad_bias, void *stream) {
+  e2f_status st = validate_linear(p, out_dtype);
+  if (st != E2F_OK) return st;
+  if (!stride_ok(ldg, p->N) || (grad_x && !stride_ok(ldgx, p->K)) || (grad_W && !stride_ok(ldgw, p->K)))
+    return E2F_ERR_INVALID_ARG;
+  if (p->M > 0 && !grad_out) return E2F_ERR_INVALID_ARG;
+  for (const void *o : {(const void *)grad_x, (const void *)grad_W, (const void *)grad_bias})
+    if (o && (o == p->x || o == p->W || o == p->bias || o == grad_out)) return E2F_ERR_INVALID_ARG;
+  if (!aligned_elem(grad_out, out_dtype) || !aligned_elem(grad_x, p->dtype) || !aligned_elem(grad_W, p->dtype) ||
+      !aligned_elem(grad_bias, E2F_F32))
+    return E2F_ERR_INVALID_ARG;
+  return linear_backward_impl(p, grad_out, ldg, out_dtype, grad_x, ldgx, grad_W, ldgw, grad_bias,
+                              static_cast<cudaStream_t>(stream));
 }
 
 e2f_status e2f_stream_status(void *stream) {

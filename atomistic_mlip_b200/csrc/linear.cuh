@@ -1,0 +1,80 @@
+// Shared parts of the linear layer's kernels: the product's description, the
+// epilogue applied to its accumulators, activations.
+#pragma once
+
+#include "common.cuh"
+#include "tc_common.cuh"
+
+namespace e2f {
+namespace lin {
+
+// What becomes of an accumulator v of row m, column n.
+constexpr int MODE_OUT = 0;    // out = act(v + bias) + extra        (extra: the residual, may be absent)
+constexpr int MODE_DZ = 1;     // out = act'(v + bias) * extra       (extra: dL/dout; out may be absent)
+constexpr int MODE_PART = 2;   // partial sum of a split contraction, fp32 [split][M][N]
+
+struct Epi {
+  int mode, act;
+  const float *bias;
+  const void *extra;
+  long long lde;
+  int etype;
+  void *out;
+  long long ldo;
+  int otype;
+  float *colpart;   // MODE_DZ: column sums of out per row block, fp32 [row blocks][N], or absent
+};
+
+// D[m][n] = sum_k A(m, k) B(n, k).  K-major: A(m, k) = A[m lda + k]; M-major:
+// A(m, k) = A[k lda + m]; the same for B.
+struct Gemm {
+  const void *A, *B;
+  long long lda, ldb;
+  int M, N, K;
+  int kper;          // contraction blocks (of BK) per split
+  float *part;       // MODE_PART
+  Epi e;
+};
+
+// z / (1 + e^-z); e^-z = inf gives -0
+__device__ __forceinline__ float silu(float z) { return z / (1.f + expf(-z)); }
+__device__ __forceinline__ float silu_grad(float z) {
+  const float s = 1.f / (1.f + expf(-z));
+  return s * (1.f + z * (1.f - s));
+}
+// the normal distribution function by erfc: no cancellation for negative z
+__device__ __forceinline__ float gelu(float z) { return 0.5f * z * erfcf(-0.70710678f * z); }
+__device__ __forceinline__ float gelu_grad(float z) {
+  return 0.5f * erfcf(-0.70710678f * z) + 0.39894228f * z * expf(-0.5f * z * z);
+}
+__device__ __forceinline__ float act_fwd(int act, float z) {
+  return act == E2F_ACT_SILU ? silu(z) : act == E2F_ACT_GELU ? gelu(z) : z;
+}
+__device__ __forceinline__ float act_bwd(int act, float z) {
+  return act == E2F_ACT_SILU ? silu_grad(z) : act == E2F_ACT_GELU ? gelu_grad(z) : 1.f;
+}
+
+__device__ __forceinline__ float load_as(const void *p, int type, size_t i) {
+  return type == E2F_F32 ? static_cast<const float *>(p)[i] : to_f(static_cast<const __nv_bfloat16 *>(p)[i]);
+}
+__device__ __forceinline__ void store_as(void *p, int type, size_t i, float v) {
+  if (type == E2F_F32) static_cast<float *>(p)[i] = v;
+  else static_cast<__nv_bfloat16 *>(p)[i] = __float2bfloat16_rn(v);
+}
+
+// One element through the epilogue; returns what MODE_DZ adds to its column's sum.
+__device__ __forceinline__ float epi_elem(const Epi &e, long long m, int n, float v, float bias) {
+  v += bias;
+  if (e.mode == MODE_OUT) {
+    v = act_fwd(e.act, v);
+    if (e.extra) v += load_as(e.extra, e.etype, (size_t)(m * e.lde) + n);
+    store_as(e.out, e.otype, (size_t)(m * e.ldo) + n, v);
+    return 0.f;
+  }
+  v = act_bwd(e.act, v) * load_as(e.extra, e.etype, (size_t)(m * e.lde) + n);
+  if (e.out) store_as(e.out, e.otype, (size_t)(m * e.ldo) + n, v);
+  return v;
+}
+
+}  // namespace lin
+}  // namespace e2f

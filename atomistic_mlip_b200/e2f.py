@@ -51,6 +51,12 @@ class BlockWeights(ctypes.Structure):
                 ("gamma2", ctypes.c_void_p), ("Wa", ctypes.c_void_p), ("Wb", _P7), ("Wd", _P7)]
 
 
+class Linear(ctypes.Structure):
+    _fields_ = [("dtype", ctypes.c_int32), ("act", ctypes.c_int32), ("M", ctypes.c_int64), ("K", ctypes.c_int32),
+                ("N", ctypes.c_int32), ("x", ctypes.c_void_p), ("ldx", ctypes.c_int64), ("W", ctypes.c_void_p),
+                ("ldw", ctypes.c_int64), ("bias", ctypes.c_void_p)]
+
+
 # name -> (restype, argtypes); must match include/e2f.h
 SIGNATURES = {
     "e2f_status_string": (ctypes.c_char_p, [ctypes.c_int32]),
@@ -83,6 +89,11 @@ SIGNATURES = {
     "e2f_embed_backward": (ctypes.c_int32, [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p,
                                             ctypes.c_int32, ctypes.c_int64, ctypes.c_int32, ctypes.c_float,
                                             ctypes.c_int32, ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p]),
+    "e2f_linear_forward": (ctypes.c_int32, [ctypes.POINTER(Linear), ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p,
+                                            ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p]),
+    "e2f_linear_backward": (ctypes.c_int32, [ctypes.POINTER(Linear), ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32,
+                                             ctypes.c_void_p, ctypes.c_int64, ctypes.c_void_p, ctypes.c_int64,
+                                             ctypes.c_void_p, ctypes.c_void_p]),
     "e2f_stream_status": (ctypes.c_int32, [ctypes.c_void_p]),
     "e2f_wigner_d": (ctypes.c_int32, [ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_void_p,
                                       ctypes.c_void_p]),
@@ -471,6 +482,88 @@ def embed_backward(ids, grad_out, V: int, scale: float = 1.0, grad_table=None, a
                                         1 if accumulate else 0, s)
     _check(code, "e2f_embed_backward")
     return grad_table
+
+
+ACT = {"none": 0, "silu": 1, "gelu": 2}
+
+
+def _ld(t, rows: int, cols: int, what: str) -> int:
+    """Row stride of a 2-D tensor whose rows are contiguous."""
+    if t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols:
+        raise ValueError(f"{what} has shape {tuple(t.shape)}, expected {(rows, cols)}")
+    s0, s1 = t.stride()
+    if s1 != 1 and cols > 1:
+        raise ValueError(f"the rows of {what} are not contiguous")
+    if rows <= 1:
+        return cols
+    if s0 < cols:
+        raise ValueError(f"the rows of {what} overlap")
+    return s0
+
+
+def _linear_struct(x, W, bias, act: str):
+    _need(x.dim() == 2 and W.dim() == 2, "x and W must be [M, K] and [N, K]")
+    M, (N, K) = int(x.shape[0]), W.shape
+    code = _code(x, "x", "f")
+    _need(W.dtype == x.dtype, f"W has type {W.dtype}, x {x.dtype}")
+    _need(act in ACT, f"act must be one of {sorted(ACT)}")
+    if bias is not None:
+        _need(bias.dtype == _torch().float32 and bias.shape == (N,) and bias.is_contiguous(),
+              f"bias must be contiguous float32 [{N}]")
+    return Linear(code, ACT[act], M, K, N, x.data_ptr(), _ld(x, M, K, "x"), W.data_ptr(), _ld(W, N, K, "W"),
+                  None if bias is None else bias.data_ptr()), M, K, N
+
+
+def linear_forward(x, W, bias=None, residual=None, act: str = "none", out=None, out_dtype=None, stream=None):
+    """act(x W^T + bias) + residual [M, N].  x [M, K] and W [N, K] float32 or
+    bfloat16 with any row stride (x may be features[:, 0] of [M, Q, K]), bias
+    float32 [N], act "none", "silu" or "gelu"; residual has the output's type
+    (x's unless given by out_dtype or out) and may be out itself."""
+    torch = _torch()
+    p, M, K, N = _linear_struct(x, W, bias, act)
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype or x.dtype, device=x.device)
+    else:
+        _need(out_dtype is None or out.dtype == out_dtype, "out has another type than out_dtype")
+    ldo, ldr = _ld(out, M, N, "out"), N
+    if residual is not None:
+        ldr = _ld(residual, M, N, "residual")
+        _need(residual.dtype == out.dtype, f"residual has type {residual.dtype}, the output {out.dtype}")
+    with _On(stream, x=x, W=W, bias=bias, residual=residual, out=out) as s:
+        code = lib().e2f_linear_forward(ctypes.byref(p), _ptr(residual), ldr, _ptr(out), ldo, _code(out, "out", "f"), s)
+    _check(code, "e2f_linear_forward")
+    return out
+
+
+def linear_backward(x, W, grad_out, bias=None, act: str = "none", need_x: bool = True, need_W: bool = True,
+                    need_bias: Optional[bool] = None, grad_x=None, grad_W=None, stream=None):
+    """(grad_x, grad_W, grad_bias) of sum(grad_out * linear_forward(x, W, bias,
+    act=act)): the first two in x's type, grad_bias float32; None where not
+    needed (grad_bias: needed if there is a bias, unless told).  grad_x and
+    grad_W may be given, with any row stride.  The residual's gradient is
+    grad_out itself."""
+    torch = _torch()
+    p, M, K, N = _linear_struct(x, W, bias, act)
+    ldg = _ld(grad_out, M, N, "grad_out")
+    if need_bias is None:
+        need_bias = bias is not None
+    gb = torch.empty((N,), dtype=torch.float32, device=x.device) if need_bias else None
+    if grad_x is None and need_x:
+        grad_x = torch.empty((M, K), dtype=x.dtype, device=x.device)
+    if grad_W is None and need_W:
+        grad_W = torch.empty((N, K), dtype=x.dtype, device=x.device)
+    ldgx = ldgw = K
+    if grad_x is not None:
+        ldgx = _ld(grad_x, M, K, "grad_x")
+        _need(grad_x.dtype == x.dtype, f"grad_x has type {grad_x.dtype}, x {x.dtype}")
+    if grad_W is not None:
+        ldgw = _ld(grad_W, N, K, "grad_W")
+        _need(grad_W.dtype == x.dtype, f"grad_W has type {grad_W.dtype}, x {x.dtype}")
+    with _On(stream, x=x, W=W, bias=bias, grad_out=grad_out, grad_x=grad_x, grad_W=grad_W) as s:
+        code = lib().e2f_linear_backward(ctypes.byref(p), _ptr(grad_out), ldg, _code(grad_out, "grad_out", "f"),
+                                         _ptr(grad_x), ldgx, _ptr(grad_W), ldgw, _ptr(gb), s)
+    _check(code, "e2f_linear_backward")
+    return grad_x, grad_W, gb
 
 
 def project_qkv(x, w: DeviceWeights, stream=None):

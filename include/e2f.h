@@ -362,6 +362,57 @@ E2F_API e2f_status e2f_embed_backward(const void *ids, int32_t id_type, int64_t 
                                       int64_t V, int32_t D, float scale, int32_t Q, float *grad_table,
                                       int32_t accumulate, void *stream);
 
+#define E2F_ACT_NONE 0
+#define E2F_ACT_SILU 1   /* z / (1 + e^-z) */
+#define E2F_ACT_GELU 2   /* z Phi(z), Phi the normal distribution function */
+
+typedef struct e2f_linear {
+  int32_t dtype;       /* E2F_F32 or E2F_BF16: type of x and W */
+  int32_t act;         /* E2F_ACT_*: smooth ones only, so that forces are continuous */
+  int64_t M;           /* rows, 0 .. 2^31 - 1 */
+  int32_t K, N;        /* inputs and outputs, 1 .. 2^20 */
+  const void *x;       /* device [M][K], row m at x + m ldx */
+  int64_t ldx;         /* elements from row to row, >= K: Q C reads the l = 0 rows of [M][Q][C] in place */
+  const void *W;       /* device [N][K] (out x in), row n at W + n ldw */
+  int64_t ldw;         /* >= K */
+  const float *bias;   /* device fp32 [N], or NULL */
+} e2f_linear;
+
+/*
+ * e2f_linear_forward -- out = act(x W^T + bias) + residual.
+ *
+ *   residual  device [M][N], row stride ldr >= N, or NULL; `out_dtype`.  It
+ *             may be `out` itself with ldr = ldo.
+ *   out       device [M][N], row stride ldo >= N, `out_dtype` (either type
+ *             for either dtype); elements between the rows are left alone.
+ * bf16 products are accumulated in fp32; E2F_F32 products are those of an
+ * fp32 multiply-add (tensor cores, three bf16 terms per operand).  The sum,
+ * bias, activation and residual are formed in fp32 and rounded once.
+ * Pointers need only their element's alignment, strides any value (16-byte
+ * aligned pointers and rows run fastest).  out may overlap no input but the
+ * residual.  Fully asynchronous.
+ */
+E2F_API e2f_status e2f_linear_forward(const e2f_linear *p, const void *residual, int64_t ldr, void *out, int64_t ldo,
+                                      int32_t out_dtype, void *stream);
+
+/*
+ * e2f_linear_backward -- gradients of sum(grad_out * e2f_linear_forward(p)).
+ *
+ *   grad_out   device [M][N], row stride ldg >= N, `out_dtype`: dL/dout (and
+ *              so dL/dresidual).
+ *   grad_x     device [M][K], row stride ldgx >= K, p->dtype, or NULL.
+ *   grad_W     device [N][K], row stride ldgw >= K, p->dtype, or NULL.
+ *   grad_bias  device fp32 [N], or NULL.
+ * With z = x W^T + bias formed again and dz = grad_out act'(z): grad_x =
+ * dz W, grad_W = dz^T x, grad_bias = the column sums of dz (fp32).  For
+ * E2F_BF16 dz is rounded to bf16 as an operand of the products.  All outputs
+ * are fully overwritten (M = 0: grad_W and grad_bias are zeros) and repeat
+ * bit for bit.  No output may overlap an input.  Fully asynchronous.
+ */
+E2F_API e2f_status e2f_linear_backward(const e2f_linear *p, const void *grad_out, int64_t ldg, int32_t out_dtype,
+                                       void *grad_x, int64_t ldgx, void *grad_W, int64_t ldgw, float *grad_bias,
+                                       void *stream);
+
 /*
  * e2f_stream_status -- synchronise `stream`, then return (and clear) any
  * error latched by a kernel of this library on the current device

@@ -59,3 +59,52 @@ def test_embed_binding():
                 lambda: e2f.embed_backward(ids, torch.zeros(4, 6), 5)):
         with pytest.raises(ValueError):
             bad()
+
+
+def _lin(dtype=0, act=1, M=4, K=8, N=6, x=64, ldx=8, W=128, ldw=8, bias=None):
+    return ctypes.byref(e2f.Linear(dtype, act, M, K, N, x, ldx, W, ldw, bias))
+
+
+def test_linear_abi(lib):
+    f, b = lib.e2f_linear_forward, lib.e2f_linear_backward
+    o = ctypes.c_void_p(1024)
+
+    def fwd(p=None, r=None, ldr=6, out=o, ldo=6, ot=0):
+        return f(p or _lin(), r, ldr, out, ldo, ot, None)
+
+    def bwd(p=None, dy=ctypes.c_void_p(512), ldg=6, ot=0, gx=o, ldgx=8, gw=ctypes.c_void_p(2048), ldgw=8, gb=None):
+        return b(p or _lin(), dy, ldg, ot, gx, ldgx, gw, ldgw, gb, None)
+
+    assert f(None, None, 6, o, 6, 0, None) == 1
+    for call in (fwd, bwd):
+        assert call(p=_lin(dtype=2)) == 4 and call(p=_lin(act=3)) == 4 and call(ot=2) == 4
+        assert call(p=_lin(M=-1)) == 1 and call(p=_lin(M=1 << 31)) == 1
+        assert call(p=_lin(K=0)) == 1 and call(p=_lin(N=0)) == 1
+        assert call(p=_lin(K=(1 << 20) + 1, ldx=1 << 21, ldw=1 << 21)) == 4
+        assert call(p=_lin(ldx=7)) == 1 and call(p=_lin(ldw=7)) == 1 and call(p=_lin(ldx=1 << 40)) == 1
+        assert call(p=_lin(x=None)) == 1 and call(p=_lin(W=None)) == 1
+        assert call(p=_lin(x=66)) == 1 and call(p=_lin(dtype=1, W=65)) == 1 and call(p=_lin(bias=66)) == 1
+    assert fwd(out=None) == 1 and fwd(ldo=5) == 1 and fwd(r=ctypes.c_void_p(4096), ldr=5) == 1
+    assert fwd(out=ctypes.c_void_p(64)) == 1 and fwd(out=ctypes.c_void_p(128)) == 1      # x, W as the output
+    assert fwd(r=o, ldr=7) == 1                                                          # in place, other stride
+    assert fwd(out=ctypes.c_void_p(1026)) == 1 and fwd(r=ctypes.c_void_p(4098)) == 1
+    assert fwd(p=_lin(M=0, x=None, W=None), out=None) == 0
+    assert bwd(dy=None) == 1 and bwd(ldg=5) == 1 and bwd(ldgx=7) == 1 and bwd(ldgw=7) == 1
+    assert bwd(gx=ctypes.c_void_p(512)) == 1 and bwd(gw=ctypes.c_void_p(128)) == 1
+    assert bwd(gx=ctypes.c_void_p(1026)) == 1 and bwd(gb=ctypes.c_void_p(1026)) == 1
+
+
+def test_linear_binding():
+    x, W, dy = torch.zeros(4, 8), torch.zeros(6, 8), torch.zeros(4, 6)
+    f, b = e2f.linear_forward, e2f.linear_backward
+    for bad in (lambda: f(x, W),                                             # not on a GPU
+                lambda: f(x.double(), W.double()), lambda: f(x, W.bfloat16()), lambda: f(x, torch.zeros(6, 9)),
+                lambda: f(x[None], W), lambda: f(x, W, act="relu"), lambda: f(x, W, bias=torch.zeros(5)),
+                lambda: f(x, W, bias=torch.zeros(6).bfloat16()), lambda: f(torch.zeros(8, 4).t(), W),
+                lambda: f(torch.zeros(1, 8).expand(4, 8), W), lambda: f(x, W, residual=torch.zeros(4, 5)),
+                lambda: f(x, W, residual=torch.zeros(4, 6).bfloat16()), lambda: f(x, W, out=torch.zeros(3, 6)),
+                lambda: f(x, W, out=torch.zeros(4, 6), out_dtype=torch.bfloat16), lambda: f(x, W, out_dtype=torch.half),
+                lambda: b(x, W, dy), lambda: b(x, W, torch.zeros(4, 5)), lambda: b(x, W, dy.double()),
+                lambda: b(x, W, dy, grad_x=torch.zeros(4, 9)), lambda: b(x, W, dy, grad_W=torch.zeros(6, 8).bfloat16())):
+        with pytest.raises(ValueError):
+            bad()
