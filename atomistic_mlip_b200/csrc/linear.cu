@@ -20,6 +20,10 @@
 namespace e2f {
 namespace lin {
 
+// linear_tma.cu
+bool tma_operand(const void *p, long long ld);
+template <bool AMN, bool BMN> e2f_status gemm_tma(const Gemm &g, int splits, int bn, int sms, cudaStream_t s);
+
 constexpr int BM = 128, BN = 128, BK = 64, NT = 256;
 constexpr int TILE_BYTES = 128 * BK * 2;     // one 128 x 64 bf16 operand tile
 constexpr int EPITCH = BN + 1;               // accumulator tile in shared memory, floats per row
@@ -351,6 +355,17 @@ template <typename T, bool AMN, bool BMN> static e2f_status launch_staged(const 
 // Row blocks whose column sums a MODE_DZ product leaves (upper bound).
 static int64_t colpart_rows(int64_t M) { return (M + FROWS - 1) / FROWS; }
 
+template <typename T, bool AMN, bool BMN> struct Path {
+  static bool tma(const Gemm &) { return false; }
+  static e2f_status run_tma(const Gemm &, int, int, int, cudaStream_t) { return E2F_ERR_UNSUPPORTED; }
+};
+template <bool AMN, bool BMN> struct Path<__nv_bfloat16, AMN, BMN> {
+  static bool tma(const Gemm &g) { return tma_operand(g.A, g.lda) && tma_operand(g.B, g.ldb); }
+  static e2f_status run_tma(const Gemm &g, int splits, int bn, int sms, cudaStream_t s) {
+    return gemm_tma<AMN, BMN>(g, splits, bn, sms, s);
+  }
+};
+
 // A product with its epilogue.  rows_out: row blocks written to e.colpart.
 template <typename T, bool AMN, bool BMN>
 static e2f_status run_gemm(Gemm g, cudaStream_t s, int *rows_out = nullptr) {
@@ -365,17 +380,27 @@ static e2f_status run_gemm(Gemm g, cudaStream_t s, int *rows_out = nullptr) {
   if (tiles < sms && nkb >= 8) splits = (int)std::min<long long>(sms / tiles, nkb / 4);
   g.kper = (nkb + splits - 1) / splits;
   splits = (nkb + g.kper - 1) / g.kper;
-  if (rows_out) *rows_out = mt;
-  if (splits == 1) return launch_staged<T, AMN, BMN>(g, dim3(mt, nt, 1), s);
+  const bool tma = Path<T, AMN, BMN>::tma(g);
+  // TMA path: 128 x 256 tiles feed the tensor core at its full rate; 128 x 128
+  // where the wider ones would leave more of the last wave idle.
+  int bn = BN;
+  if (tma && g.N > BN && splits == 1) {
+    const long long nt2 = (g.N + 2 * BN - 1) / (2 * BN);
+    const long long w1 = (tiles + sms - 1) / sms, w2 = (mt * nt2 + sms - 1) / sms;
+    if (9 * w2 <= 5 * w1) bn = 2 * BN;
+  }
   const Epi e = g.e;
   Scratch ws;
-  E2F_CUDA_TRY(ws.alloc(sizeof(float) * (size_t)splits * g.M * g.N, s));
-  g.part = ws.as<float>();
-  g.e.mode = MODE_PART;
-  e2f_status st = launch_staged<T, AMN, BMN>(g, dim3(mt, nt, splits), s);
-  if (st != E2F_OK) return st;
+  if (splits > 1) {
+    E2F_CUDA_TRY(ws.alloc(sizeof(float) * (size_t)splits * g.M * g.N, s));
+    g.part = ws.as<float>();
+    g.e.mode = MODE_PART;
+  }
+  e2f_status st = tma ? Path<T, AMN, BMN>::run_tma(g, splits, bn, sms, s)
+                      : launch_staged<T, AMN, BMN>(g, dim3(mt, nt, splits), s);
+  if (rows_out) *rows_out = tma || splits > 1 ? (int)colpart_rows(g.M) : mt;
+  if (st != E2F_OK || splits == 1) return st;
   dim3 fg((unsigned)((g.M + FROWS - 1) / FROWS), (unsigned)nt);
-  if (rows_out) *rows_out = (int)fg.x;
   E2F_LAUNCH(finish_kernel, fg, NT, 0, s, g.part, splits, g.M, g.N, e);
   return E2F_OK;
 }

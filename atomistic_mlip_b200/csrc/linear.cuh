@@ -36,16 +36,18 @@ struct Gemm {
   Epi e;
 };
 
-// z / (1 + e^-z); e^-z = inf gives -0
-__device__ __forceinline__ float silu(float z) { return z / (1.f + expf(-z)); }
+// sigma(z) = 1 / (1 + e^-z) by the special-function unit (2 instructions of it):
+// good to about 2^-21, and e^-z = inf gives 0
+__device__ __forceinline__ float sigmoid(float z) { return __fdividef(1.f, 1.f + __expf(-z)); }
+__device__ __forceinline__ float silu(float z) { return z * sigmoid(z); }
 __device__ __forceinline__ float silu_grad(float z) {
-  const float s = 1.f / (1.f + expf(-z));
+  const float s = sigmoid(z);
   return s * (1.f + z * (1.f - s));
 }
 // the normal distribution function by erfc: no cancellation for negative z
 __device__ __forceinline__ float gelu(float z) { return 0.5f * z * erfcf(-0.70710678f * z); }
 __device__ __forceinline__ float gelu_grad(float z) {
-  return 0.5f * erfcf(-0.70710678f * z) + 0.39894228f * z * expf(-0.5f * z * z);
+  return 0.5f * erfcf(-0.70710678f * z) + 0.39894228f * z * __expf(-0.5f * z * z);
 }
 __device__ __forceinline__ float act_fwd(int act, float z) {
   return act == E2F_ACT_SILU ? silu(z) : act == E2F_ACT_GELU ? gelu(z) : z;

@@ -1,0 +1,463 @@
+// bf16 products of the linear layers with TMA-fed tensor cores: the path for
+// operands whose rows start on 16-byte boundaries.
+//
+// A persistent CTA per SM walks output tiles of 128 x BN (BN = 128 or 256).
+// Warp 0 loads 64-wide operand slices by TMA into a ring of stages (128-byte
+// swizzle; rows and columns outside the matrices arrive as zeros), warp 1
+// issues the MMAs into one of two accumulators in tensor memory, warps 2-9
+// run the epilogue of the other one meanwhile: TMEM -> shared memory -> rows,
+// so that residual, dL/dout and results move in 16-byte pieces of contiguous
+// rows.
+//
+// The tensor core's fp32 accumulation truncates: a chain of s MMAs (16
+// products each) leaves a relative error near s * 1e-8 (measured: 2.7e-6 at
+// 256).  Where fp32 results hang on it, LONGK ends the chain every KCHUNK
+// blocks and the epilogue warps add the pieces in registers, rounded to
+// nearest.
+#include <cuda.h>
+
+#include <algorithm>
+
+#include "linear.cuh"
+
+namespace e2f {
+namespace lin {
+
+namespace tma {
+
+constexpr int BM = 128, BK = 64;
+constexpr int NT = 320;
+constexpr int EPI_WARPS = 8;
+constexpr int KCHUNK = 16;                       // blocks of 64 per chain (LONGK)
+constexpr int STAGING = EPI_WARPS * 32 * 32 * 4;
+constexpr int RING = 196608;
+template <int BN> constexpr int stage_bytes() { return (BM + BN) * BK * 2; }
+template <int BN> constexpr int stages() { return RING / stage_bytes<BN>(); }
+constexpr size_t SMEM = RING + STAGING + 256 + 1024;
+
+struct Args {
+  Gemm g;
+  int mt, nt, tiles, nkb;   // tiles: mt * nt * splits
+  int vec;                  // 16-byte rows of out and extra, N a multiple of 8
+  int *err;
+};
+
+__device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.shared::cta.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+          tc::smem_addr(dst)),
+      "l"(map), "r"(x), "r"(y), "r"(tc::smem_addr(bar))
+      : "memory");
+}
+
+// One operand slice: R rows (m or n) from r0, 64 contraction columns from k0.
+// K-major: one box of R rows x 64; MN-major: boxes of 64 contraction rows x 64.
+template <bool MN, int R>
+__device__ __forceinline__ void load_slice(uint8_t *dst, const CUtensorMap *map, int r0, int k0, uint64_t *bar) {
+  if (!MN) {
+    tma_load_2d(dst, map, k0, r0, bar);
+  } else {
+#pragma unroll
+    for (int j = 0; j < R / 64; ++j) tma_load_2d(dst + j * 8192, map, r0 + 64 * j, k0, bar);
+  }
+}
+
+template <bool MN> __device__ __forceinline__ uint64_t slice_desc(uint32_t saddr, int k) {
+  const uint32_t a = saddr + (MN ? k * 128 : k * 2);
+  return tc::smem_desc(a, MN ? 8192 : 16, 1024) | (uint64_t)2 << 61;
+}
+
+struct Tile {
+  int m0, n0, split, kb0, kb1, mi;
+};
+// Consecutive tiles share their rows of A (up to 16 column tiles, then the
+// next row tile): a wave of CTAs reads few rows of A and one band of B.
+template <int BN> __device__ __forceinline__ Tile tile_of(const Args &a, int i) {
+  Tile t;
+  const int per = a.mt * a.nt;
+  t.split = i / per;
+  int r = i - t.split * per;
+  const int band = a.mt * 16, b = r / band;
+  r -= b * band;
+  const int w = min(16, a.nt - 16 * b);
+  t.mi = r / w;
+  t.m0 = t.mi * BM;
+  t.n0 = (16 * b + r - t.mi * w) * BN;
+  t.kb0 = t.split * a.g.kper;
+  t.kb1 = min(t.kb0 + a.g.kper, a.nkb);
+  return t;
+}
+
+__device__ __forceinline__ void unpack8(const uint4 &a, const uint4 &b, int type, float (&v)[8]) {
+  if (type == E2F_F32) {
+    v[0] = __uint_as_float(a.x); v[1] = __uint_as_float(a.y); v[2] = __uint_as_float(a.z); v[3] = __uint_as_float(a.w);
+    v[4] = __uint_as_float(b.x); v[5] = __uint_as_float(b.y); v[6] = __uint_as_float(b.z); v[7] = __uint_as_float(b.w);
+  } else {
+    v[0] = __uint_as_float(a.x << 16); v[1] = __uint_as_float(a.x & 0xffff0000u);
+    v[2] = __uint_as_float(a.y << 16); v[3] = __uint_as_float(a.y & 0xffff0000u);
+    v[4] = __uint_as_float(a.z << 16); v[5] = __uint_as_float(a.z & 0xffff0000u);
+    v[6] = __uint_as_float(a.w << 16); v[7] = __uint_as_float(a.w & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void store8(void *p, int type, size_t i, const float (&v)[8]) {
+  if (type == E2F_F32) {
+    float4 *q = reinterpret_cast<float4 *>(static_cast<float *>(p) + i);
+    q[0] = make_float4(v[0], v[1], v[2], v[3]);
+    q[1] = make_float4(v[4], v[5], v[6], v[7]);
+  } else {
+    *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p) + i) =
+        make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+  }
+}
+
+// FULL_EPI: bias, activation, extra (MODE_OUT, MODE_DZ); else accumulators as
+// they are to out or to the partial sums.
+template <bool AMN, bool BMN, int BN, bool LONGK, bool FULL_EPI>
+__global__ void __launch_bounds__(NT, 1)
+gemm_tma_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tbm,
+                const __grid_constant__ Args a) {
+  using namespace tc;
+  constexpr int ST = stages<BN>(), SB = stage_bytes<BN>(), ABYTES = BM * BK * 2;
+  constexpr uint32_t LIMIT = 1u << 26;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
+  float *staging = reinterpret_cast<float *>(smem + RING);
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + RING + STAGING), *empty = full + ST, *tfull = empty + ST,
+           *tempty = tfull + 2;
+  __shared__ uint32_t tslot;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < ST; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
+    for (int i = 0; i < 2; ++i) { mbar_init(&tfull[i], 1); mbar_init(&tempty[i], EPI_WARPS); }
+    mbar_fence_init();
+  }
+  __syncthreads();
+  if (warp == 1) { tmem_alloc(&tslot, 2 * BN); tmem_relinquish(); }
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tslot;
+
+  if (warp == 0) {
+    if (lane == 0) {
+      int s = 0;
+      uint32_t ph = 1;   // the first pass over the ring finds it empty
+      bool ok = true;
+      for (int i = blockIdx.x; i < a.tiles && ok; i += gridDim.x) {
+        const Tile t = tile_of<BN>(a, i);
+        for (int kb = t.kb0; kb < t.kb1; ++kb) {
+          ok = mbar_wait(&empty[s], ph, LIMIT);
+          if (!ok) break;
+          mbar_arrive_expect_tx(&full[s], SB);
+          load_slice<AMN, BM>(smem + s * SB, &ta, t.m0, kb * BK, &full[s]);
+          load_slice<BMN, BN>(smem + s * SB + ABYTES, &tbm, t.n0, kb * BK, &full[s]);
+          if (++s == ST) { s = 0; ph ^= 1; }
+        }
+      }
+      if (!ok) atomicExch(a.err, E2F_ERR_TIMEOUT);
+    }
+  } else if (warp == 1) {
+    if (lane == 0) {
+      int s = 0, u = 0;   // ring slot, accumulator units issued
+      uint32_t ph = 0;
+      bool ok = true;
+      for (int i = blockIdx.x; i < a.tiles && ok; i += gridDim.x) {
+        const Tile t = tile_of<BN>(a, i);
+        const int nb = min(BN, (a.g.N - t.n0 + 15) & ~15);
+        const uint32_t id = idesc_bf16(128, nb, AMN, BMN);
+        for (int kc = t.kb0; kc < t.kb1 && ok; kc += LONGK ? KCHUNK : t.kb1 - t.kb0, ++u) {
+          const int ke = LONGK ? min(kc + KCHUNK, t.kb1) : t.kb1;
+          const uint32_t acc = tmem + (u & 1) * BN;
+          ok = mbar_wait(&tempty[u & 1], ((u >> 1) & 1) ^ 1, LIMIT);
+          if (!ok) break;
+          tc_fence_after();
+          for (int kb = kc; kb < ke; ++kb) {
+            ok = mbar_wait(&full[s], ph, LIMIT);
+            if (!ok) break;
+            tc_fence_after();
+            const uint32_t a0 = smem_addr(smem + s * SB), b0 = a0 + ABYTES;
+#pragma unroll
+            for (int k = 0; k < BK; k += 16)
+              mma_bf16_ss(acc, slice_desc<AMN>(a0, k), slice_desc<BMN>(b0, k), id, kb > kc || k > 0 ? 1u : 0u);
+            mma_commit(&empty[s]);
+            if (++s == ST) { s = 0; ph ^= 1; }
+          }
+          mma_commit(&tfull[u & 1]);
+        }
+      }
+      if (!ok) atomicExch(a.err, E2F_ERR_TIMEOUT);
+    }
+  } else {
+    const int ew = warp - 2, quarter = warp & 3, half = ew >> 2;   // TMEM lanes 32 quarter + .., columns half * BN / 2 + ..
+    const uint32_t tq = tmem + ((uint32_t)(32 * quarter) << 16) + half * (BN / 2);
+    float *st = staging + ew * 32 * 32;
+    const Epi &e = a.g.e;
+    constexpr int NCH = BN / 64;   // 32-column chunks of this warp
+    const int r8 = lane >> 2, cg = (lane & 3) * 8;
+    int u = 0;
+    bool ok = true;
+    for (int i = blockIdx.x; i < a.tiles && ok; i += gridDim.x) {
+      const Tile t = tile_of<BN>(a, i);
+      const int nw = t.n0 + half * (BN / 2), mw = t.m0 + 32 * quarter;
+      float acc[LONGK ? BN / 2 : 1];
+      if (LONGK) {
+#pragma unroll
+        for (int j = 0; j < BN / 2; ++j) acc[j] = 0.f;
+        for (int kc = t.kb0; kc < t.kb1; kc += KCHUNK, ++u) {
+          ok = __all_sync(0xffffffffu, mbar_wait(&tfull[u & 1], (u >> 1) & 1, LIMIT));
+          if (!ok) break;
+          tc_fence_after();
+#pragma unroll
+          for (int c = 0; c < BN / 2; c += 16) {
+            float v[16];
+            tmem_ld_32x32b_x16(tq + (u & 1) * BN + c, v);
+#pragma unroll
+            for (int j = 0; j < 16; ++j) acc[c + j] += v[j];
+          }
+          tc_fence_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&tempty[u & 1]);
+        }
+      } else {
+        ok = __all_sync(0xffffffffu, mbar_wait(&tfull[u & 1], (u >> 1) & 1, LIMIT));
+        tc_fence_after();
+      }
+      if (!ok) break;
+      // Not unrolled: the chunk's code fits the instruction cache once.
+#pragma unroll 1
+      for (int c = 0; c < NCH; ++c) {
+        const int n = nw + 32 * c;
+        if (n < a.g.N && mw < a.g.M) {
+          const bool part = !FULL_EPI && e.mode == MODE_PART;
+          const int ng = n + cg;
+          // what the epilogue reads, on its way while the accumulators move
+          uint4 x0[4], x1[4];
+          float bias = 0.f;
+          if (FULL_EPI) {
+            if (e.bias && n + lane < a.g.N) bias = __ldg(e.bias + n + lane);
+            if (a.vec && e.extra && ng < a.g.N) {
+#pragma unroll
+              for (int q = 0; q < 4; ++q) {
+                const int m = mw + 8 * q + r8;
+                if (m < a.g.M) {
+                  const size_t o = (size_t)(m * e.lde) + ng;
+                  if (e.etype == E2F_F32) {
+                    const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const float *>(e.extra) + o);
+                    x0[q] = p[0];
+                    x1[q] = p[1];
+                  } else {
+                    x0[q] = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(e.extra) + o);
+                  }
+                }
+              }
+            }
+          }
+          // lane = row: accumulators, bias, activation -> staging
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            float v[16];
+            if (LONGK) {
+#pragma unroll
+              for (int k = 0; k < NCH; ++k)
+                if (k == c) {
+#pragma unroll
+                  for (int j = 0; j < 16; ++j) v[j] = acc[LONGK ? 32 * k + 16 * h + j : 0];
+                }
+            } else {
+              tmem_ld_32x32b_x16(tq + (u & 1) * BN + 32 * c + 16 * h, v);
+            }
+            if (FULL_EPI) {
+#pragma unroll
+              for (int j = 0; j < 16; ++j) v[j] += __shfl_sync(0xffffffffu, bias, 16 * h + j);
+              if (e.mode == MODE_OUT) {
+                if (e.act == E2F_ACT_SILU) {
+#pragma unroll
+                  for (int j = 0; j < 16; ++j) v[j] = silu(v[j]);
+                } else if (e.act == E2F_ACT_GELU) {
+#pragma unroll
+                  for (int j = 0; j < 16; ++j) v[j] = gelu(v[j]);
+                }
+              } else if (e.act == E2F_ACT_SILU) {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) v[j] = silu_grad(v[j]);
+              } else {
+#pragma unroll
+                for (int j = 0; j < 16; ++j) v[j] = gelu_grad(v[j]);
+              }
+            }
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+              *reinterpret_cast<float4 *>(st + lane * 32 + (((4 * h + j) ^ (lane & 7)) << 2)) =
+                  make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+          }
+          __syncwarp();
+          if (a.vec) {
+            float cs[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j) cs[j] = 0.f;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int row = 8 * q + r8, m = mw + row;
+              if (m < a.g.M && ng < a.g.N) {
+                const float4 lo = *reinterpret_cast<const float4 *>(st + row * 32 + (((cg >> 2) ^ (row & 7)) << 2));
+                const float4 hi = *reinterpret_cast<const float4 *>(st + row * 32 + (((cg >> 2) + 1 ^ (row & 7)) << 2));
+                float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+                if (part) {
+                  store8(a.g.part, E2F_F32, ((size_t)t.split * a.g.M + m) * a.g.N + ng, v);
+                } else if (!FULL_EPI) {
+                  store8(e.out, e.otype, (size_t)(m * e.ldo) + ng, v);
+                } else {
+                  float x[8];
+                  if (e.extra) unpack8(x0[q], x1[q], e.etype, x);
+                  if (e.mode == MODE_OUT) {
+                    if (e.extra) {
+#pragma unroll
+                      for (int j = 0; j < 8; ++j) v[j] += x[j];
+                    }
+                  } else {
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                      v[j] *= x[j];
+                      cs[j] += v[j];
+                    }
+                  }
+                  if (e.out) store8(e.out, e.otype, (size_t)(m * e.ldo) + ng, v);
+                }
+              }
+            }
+            if (FULL_EPI && e.mode == MODE_DZ && e.colpart) {   // column sums of the warp's 32 rows
+#pragma unroll
+              for (int j = 0; j < 8; ++j) {
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) cs[j] += __shfl_xor_sync(0xffffffffu, cs[j], o);
+              }
+              if (lane < 4 && ng < a.g.N) store8(e.colpart, E2F_F32, (size_t)(mw >> 5) * a.g.N + ng, cs);
+            }
+          } else if (n + lane < a.g.N) {   // any alignment: lane = column
+            const int nl = n + lane;
+            float cs = 0.f;
+#pragma unroll 4
+            for (int r = 0; r < 32; ++r) {
+              const int m = mw + r;
+              if (m >= a.g.M) break;
+              float v = st[r * 32 + ((((lane >> 2) ^ (r & 7)) << 2) | (lane & 3))];
+              if (part) {
+                a.g.part[((size_t)t.split * a.g.M + m) * a.g.N + nl] = v;
+              } else {
+                if (FULL_EPI && e.extra) {
+                  const float x = load_as(e.extra, e.etype, (size_t)(m * e.lde) + nl);
+                  v = e.mode == MODE_OUT ? v + x : v * x;
+                  cs += v;
+                }
+                if (e.out) store_as(e.out, e.otype, (size_t)(m * e.ldo) + nl, v);
+              }
+            }
+            if (FULL_EPI && e.mode == MODE_DZ && e.colpart) e.colpart[(size_t)(mw >> 5) * a.g.N + nl] = cs;
+          }
+          __syncwarp();
+        }
+      }
+      if (!LONGK) {
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&tempty[u & 1]);
+        ++u;
+      }
+    }
+    if (!ok && lane == 0) atomicExch(a.err, E2F_ERR_TIMEOUT);
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 1) tmem_dealloc(tmem, 2 * BN);
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+typedef CUresult (*EncodeFn)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *, const cuuint64_t *,
+                             const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave, CUtensorMapSwizzle,
+                             CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+static EncodeFn encode_fn() {
+  static EncodeFn fn = [] {
+    void *p = nullptr;
+    cudaDriverEntryPointQueryResult q;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      p = nullptr;
+    return reinterpret_cast<EncodeFn>(p);
+  }();
+  return fn;
+}
+
+// [rows][cols] bf16, row stride ld elements; boxes of box_rows x 64 columns.
+static bool encode(CUtensorMap *m, const void *p, long long rows, long long cols, long long ld, int box_rows) {
+  const EncodeFn fn = encode_fn();
+  if (!fn) return false;
+  const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)ld * 2};
+  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, es[2] = {1, 1};
+  return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(p), dims, strides, box, es,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <bool AMN, bool BMN, int BN, bool LONGK, bool FULL_EPI>
+static e2f_status launch_epi(const CUtensorMap &ta, const CUtensorMap &tb, const Args &a, int sms, cudaStream_t s) {
+  auto k = gemm_tma_kernel<AMN, BMN, BN, LONGK, FULL_EPI>;
+  E2F_CUDA_TRY(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM));
+  E2F_LAUNCH(k, std::min(a.tiles, sms), NT, SMEM, s, ta, tb, a);
+  return E2F_OK;
+}
+
+template <bool AMN, bool BMN, int BN, bool LONGK>
+static e2f_status launch(const CUtensorMap &ta, const CUtensorMap &tb, const Args &a, int sms, cudaStream_t s) {
+  const Epi &e = a.g.e;
+  if (!AMN && !BMN && e.mode != MODE_PART && (e.mode == MODE_DZ || e.bias || e.extra || e.act != E2F_ACT_NONE))
+    return launch_epi<AMN, BMN, BN, LONGK, !AMN && !BMN>(ta, tb, a, sms, s);
+  return launch_epi<AMN, BMN, BN, LONGK, false>(ta, tb, a, sms, s);
+}
+
+}  // namespace tma
+
+bool tma_operand(const void *p, long long ld) {
+  return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)(ld * 2)) & 15) == 0;
+}
+
+// A bf16 product of aligned operands, split into `splits` parts of g.kper
+// contraction blocks (MODE_PART when there are several); bn = 128 or 256.
+template <bool AMN, bool BMN>
+e2f_status gemm_tma(const Gemm &g, int splits, int bn, int sms, cudaStream_t s) {
+  using namespace tma;
+  Args a{};
+  a.g = g;
+  a.mt = (g.M + BM - 1) / BM;
+  a.nt = (g.N + bn - 1) / bn;
+  a.nkb = (g.K + BK - 1) / BK;
+  const long long tiles = (long long)a.mt * a.nt * splits;
+  if (tiles > INT32_MAX / 2) return E2F_ERR_UNSUPPORTED;
+  a.tiles = (int)tiles;
+  a.err = device_error_flag();
+  if (!a.err) return E2F_ERR_CUDA;
+  auto rows16 = [](const void *p, long long ld, int type) {
+    return !p || ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)(ld * (type == E2F_F32 ? 4 : 2))) & 15) == 0;
+  };
+  a.vec = g.N % 8 == 0 && (g.e.mode == MODE_PART || (rows16(g.e.out, g.e.ldo, g.e.otype) && rows16(g.e.extra, g.e.lde, g.e.etype)));
+  CUtensorMap ta, tb;
+  const bool ok = (AMN ? encode(&ta, g.A, g.K, g.M, g.lda, 64) : encode(&ta, g.A, g.M, g.K, g.lda, BM)) &&
+                  (BMN ? encode(&tb, g.B, g.K, g.N, g.ldb, 64) : encode(&tb, g.B, g.N, g.K, g.ldb, bn));
+  if (!ok) {
+    set_cuda_error(cudaErrorInvalidValue, "cuTensorMapEncodeTiled");
+    return E2F_ERR_CUDA;
+  }
+  const bool fp32 = g.e.mode == MODE_PART || (g.e.mode == MODE_OUT ? g.e.otype == E2F_F32 : g.e.colpart != nullptr);
+  const bool longk = fp32 && g.kper > KCHUNK;
+  if (bn == 256)
+    return longk ? launch<AMN, BMN, 256, true>(ta, tb, a, sms, s) : launch<AMN, BMN, 256, false>(ta, tb, a, sms, s);
+  return longk ? launch<AMN, BMN, 128, true>(ta, tb, a, sms, s) : launch<AMN, BMN, 128, false>(ta, tb, a, sms, s);
+}
+template e2f_status gemm_tma<false, false>(const Gemm &, int, int, int, cudaStream_t);
+template e2f_status gemm_tma<false, true>(const Gemm &, int, int, int, cudaStream_t);
+template e2f_status gemm_tma<true, true>(const Gemm &, int, int, int, cudaStream_t);
+
+}  // namespace lin
+}  // namespace e2f
