@@ -275,62 +275,82 @@ __global__ void __launch_bounds__(NT, 1) gemm_staged_kernel(const __grid_constan
 }
 
 // ---------------------------------------------------------------------------
-// Partial sums of a split contraction added in order, then the epilogue (with
-// no partial sums: the epilogue of zero accumulators, act'(.) dy = dy).  A CTA
-// takes FROWS rows of 128 columns.
+// Partial sums of a split contraction added in a fixed order, then the
+// epilogue (with no partial sums: the epilogue of zero accumulators, act'(.) dy
+// = dy).  A CTA takes FROWS rows of 32 columns; a warp takes whole rows (one
+// element a lane) while there are few splits, else the eight warps share the
+// splits of a row.
 // ---------------------------------------------------------------------------
 constexpr int FROWS = 32;
 __global__ void __launch_bounds__(NT) finish_kernel(const float *__restrict__ part, int splits, int M, int N,
                                                     const __grid_constant__ Epi e) {
-  __shared__ float red[NT / 32][128];
+  __shared__ float red[NT / 32][33];
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int n0 = blockIdx.y * 128;
+  const int n = blockIdx.y * 32 + lane;
   const long long m0 = (long long)blockIdx.x * FROWS;
-  float csum[4];
+  const float bias = e.bias && n < N ? e.bias[n] : 0.f;
+  float csum = 0.f;
+  if (n < N) {
 #pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    csum[j] = 0.f;
-    const int n = n0 + lane + 32 * j;
-    if (n >= N) continue;
-    const float bias = e.bias ? e.bias[n] : 0.f;
-#pragma unroll
-    for (int r = warp; r < FROWS; r += NT / 32) {
-      const long long m = m0 + r;
+    for (int r = 0; r < FROWS / 8; ++r) {
+      const long long m = m0 + warp + 8 * r;
       if (m >= M) break;
       float v = 0.f;
-#pragma unroll 4
+#pragma unroll 8
       for (int s = 0; s < splits; ++s) v += part[((size_t)s * M + m) * N + n];
-      csum[j] += epi_elem(e, m, n, v, bias);
+      csum += epi_elem(e, m, n, v, bias);
     }
   }
   if (e.mode == MODE_DZ && e.colpart) {
-#pragma unroll
-    for (int j = 0; j < 4; ++j) red[warp][lane + 32 * j] = csum[j];
+    red[warp][lane] = csum;
     __syncthreads();
-    const int t = threadIdx.x;
-    if (t < 128 && n0 + t < N) {
+    if (warp == 0 && n < N) {
       float s = 0.f;
 #pragma unroll
-      for (int w = 0; w < NT / 32; ++w) s += red[w][t];
-      e.colpart[(size_t)blockIdx.x * N + n0 + t] = s;
+      for (int w = 0; w < NT / 32; ++w) s += red[w][lane];
+      e.colpart[(size_t)blockIdx.x * N + n] = s;
     }
   }
 }
 
-// Column sums of P partial rows: 32 columns a CTA, eight interleaved sums each.
+// The same for MODE_OUT, one row and 32 columns a CTA: eight interleaved sums
+// over the splits, joined in order.
+__global__ void __launch_bounds__(NT) finish_row_kernel(const float *__restrict__ part, int splits, int M, int N,
+                                                        const __grid_constant__ Epi e) {
+  __shared__ float red[NT / 32][33];
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int n = blockIdx.y * 32 + lane, m = blockIdx.x;
+  float v = 0.f;
+  if (n < N)
+#pragma unroll 8
+    for (int s = warp; s < splits; s += NT / 32) v += part[((size_t)s * M + m) * N + n];
+  red[warp][lane] = v;
+  __syncthreads();
+  if (warp == 0 && n < N) {
+#pragma unroll
+    for (int w = 1; w < NT / 32; ++w) v += red[w][lane];
+    epi_elem(e, m, n, v, e.bias ? e.bias[n] : 0.f);
+  }
+}
+
+// Column sums of P partial rows: a CTA takes 32 columns and CROWS rows, eight
+// interleaved sums joined in order; called again on its own partial rows until
+// one is left.
+constexpr int CROWS = 128;
 __global__ void __launch_bounds__(256) colsum_kernel(const float *__restrict__ part, int P, int N, float *__restrict__ out) {
   __shared__ float red[8][32];
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, n = blockIdx.x * 32 + lane;
+  const int p0 = blockIdx.y * CROWS, p1 = min(p0 + CROWS, P);
   float s = 0.f;
   if (n < N)
 #pragma unroll 8
-    for (int p = w; p < P; p += 8) s += part[(size_t)p * N + n];
+    for (int p = p0 + w; p < p1; p += 8) s += part[(size_t)p * N + n];
   red[w][lane] = s;
   __syncthreads();
   if (w == 0 && n < N) {
 #pragma unroll
     for (int j = 1; j < 8; ++j) s += red[j][lane];
-    out[n] = s;
+    out[(size_t)blockIdx.y * N + n] = s;
   }
 }
 
@@ -400,8 +420,13 @@ static e2f_status run_gemm(Gemm g, cudaStream_t s, int *rows_out = nullptr) {
                       : launch_staged<T, AMN, BMN>(g, dim3(mt, nt, splits), s);
   if (rows_out) *rows_out = tma || splits > 1 ? (int)colpart_rows(g.M) : mt;
   if (st != E2F_OK || splits == 1) return st;
-  dim3 fg((unsigned)((g.M + FROWS - 1) / FROWS), (unsigned)nt);
-  E2F_LAUNCH(finish_kernel, fg, NT, 0, s, g.part, splits, g.M, g.N, e);
+  const unsigned fy = (unsigned)((g.N + 31) / 32);
+  if (e.mode == MODE_OUT && splits > 8) {
+    E2F_LAUNCH(finish_row_kernel, dim3((unsigned)g.M, fy), NT, 0, s, g.part, splits, g.M, g.N, e);
+  } else {
+    dim3 fg((unsigned)((g.M + FROWS - 1) / FROWS), fy);
+    E2F_LAUNCH(finish_kernel, fg, NT, 0, s, g.part, splits, g.M, g.N, e);
+  }
   return E2F_OK;
 }
 
@@ -434,7 +459,9 @@ static e2f_status backward(const e2f_linear &p, const void *dy, int64_t ldg, int
   const long long lddz = (N + 7) & ~7;
   auto up = [](size_t b) { return (b + 255) & ~(size_t)255; };
   const size_t zb = own && prod ? up(sizeof(T) * (size_t)M * lddz) : 0;
-  const size_t cb = gb ? sizeof(float) * (size_t)colpart_rows(M) * N : 0;
+  // partial rows of the column sums, and one level of their sums
+  const int64_t cr = colpart_rows(M);
+  const size_t cb = gb ? sizeof(float) * (size_t)(cr + (cr + CROWS - 1) / CROWS) * N : 0;
   Scratch ws;
   if (zb + cb) E2F_CUDA_TRY(ws.alloc(zb + cb, s));
   const void *dz = dy;
@@ -452,13 +479,20 @@ static e2f_status backward(const e2f_linear &p, const void *dy, int64_t ldg, int
       e2f_status st = run_gemm<T, false, false>(g, s, &crows);
       if (st != E2F_OK) return st;
     } else {
-      dim3 fg((unsigned)((M + FROWS - 1) / FROWS), (unsigned)((N + 127) / 128));
+      dim3 fg((unsigned)((M + FROWS - 1) / FROWS), (unsigned)((N + 31) / 32));
       g.e.bias = nullptr;
       E2F_LAUNCH(finish_kernel, fg, NT, 0, s, nullptr, 0, M, N, g.e);
       crows = (int)fg.x;
     }
     if (own && prod) { dz = ws.p; ldz = lddz; }
-    if (gb) E2F_LAUNCH(colsum_kernel, (N + 31) / 32, 256, 0, s, g.e.colpart, crows, N, gb);
+    if (gb) {
+      float *from = g.e.colpart, *to = from + (size_t)cr * N;
+      for (int P = crows;; std::swap(from, to)) {
+        const int q = (P + CROWS - 1) / CROWS;
+        E2F_LAUNCH(colsum_kernel, dim3((N + 31) / 32, q), 256, 0, s, from, P, N, q == 1 ? gb : to);
+        if ((P = q) == 1) break;
+      }
+    }
   }
   if (gx) {
     Gemm g{};

@@ -44,10 +44,32 @@ __device__ __forceinline__ float silu_grad(float z) {
   const float s = sigmoid(z);
   return s * (1.f + z * (1.f - s));
 }
-// the normal distribution function by erfc: no cancellation for negative z
-__device__ __forceinline__ float gelu(float z) { return 0.5f * z * erfcf(-0.70710678f * z); }
+// Phi(z), the normal distribution function, from Abramowitz and Stegun's
+// rational approximation 7.1.26 of erfc(x) = t (a1 + t (a2 + ...)) e^(-x^2),
+// t = 1 / (1 + p x) for x >= 0 (absolute error 1.5e-7, so 0.75e-7 in Phi), with
+// x = |z| / sqrt 2; *e gets e^(-z^2 / 2), which the gradient needs as well.
+// A third of erfcf's instructions, which bounded the epilogue (8,192 x 4,096 ->
+// 4,096: 202 us with erfcf, 178 us without any activation).
+__device__ __forceinline__ float normal_cdf(float z, float *e) {
+  const float x = 0.70710678f * fabsf(z);
+  const float t = __fdividef(1.f, fmaf(0.3275911f, x, 1.f));
+  const float ex = __expf(-x * x);
+  float q = fmaf(1.061405429f, t, -1.453152027f);
+  q = fmaf(q, t, 1.421413741f);
+  q = fmaf(q, t, -0.284496736f);
+  q = fmaf(q, t, 0.254829592f);
+  q *= 0.5f * t * ex;   // Phi(-|z|)
+  *e = ex;
+  return z < 0.f ? q : 1.f - q;
+}
+__device__ __forceinline__ float gelu(float z) {
+  float e;
+  return z * normal_cdf(z, &e);
+}
 __device__ __forceinline__ float gelu_grad(float z) {
-  return 0.5f * erfcf(-0.70710678f * z) + 0.39894228f * z * __expf(-0.5f * z * z);
+  float e;
+  const float p = normal_cdf(z, &e);
+  return fmaf(0.39894228f * z, e, p);
 }
 __device__ __forceinline__ float act_fwd(int act, float z) {
   return act == E2F_ACT_SILU ? silu(z) : act == E2F_ACT_GELU ? gelu(z) : z;

@@ -30,10 +30,11 @@ constexpr int NT = 320;
 constexpr int EPI_WARPS = 8;
 constexpr int KCHUNK = 16;                       // blocks of 64 per chain (LONGK)
 constexpr int STAGING = EPI_WARPS * 32 * 32 * 4;
+constexpr int SBIAS = EPI_WARPS * 32 * 4;
 constexpr int RING = 196608;
 template <int BN> constexpr int stage_bytes() { return (BM + BN) * BK * 2; }
 template <int BN> constexpr int stages() { return RING / stage_bytes<BN>(); }
-constexpr size_t SMEM = RING + STAGING + 256 + 1024;
+constexpr size_t SMEM = RING + STAGING + SBIAS + 256 + 1024;
 
 struct Args {
   Gemm g;
@@ -66,6 +67,10 @@ template <bool MN> __device__ __forceinline__ uint64_t slice_desc(uint32_t saddr
   const uint32_t a = saddr + (MN ? k * 128 : k * 2);
   return tc::smem_desc(a, MN ? 8192 : 16, 1024) | (uint64_t)2 << 61;
 }
+
+struct Extra {   // 4 x 8 elements of residual or dL/dout: bf16 in lo, fp32 in lo and hi
+  uint4 lo[4], hi[4];
+};
 
 struct Tile {
   int m0, n0, split, kb0, kb1, mi;
@@ -122,7 +127,7 @@ gemm_tma_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ 
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   float *staging = reinterpret_cast<float *>(smem + RING);
-  uint64_t *full = reinterpret_cast<uint64_t *>(smem + RING + STAGING), *empty = full + ST, *tfull = empty + ST,
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + RING + STAGING + SBIAS), *empty = full + ST, *tfull = empty + ST,
            *tempty = tfull + 2;
   __shared__ uint32_t tslot;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -192,6 +197,9 @@ gemm_tma_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ 
     const uint32_t tq = tmem + ((uint32_t)(32 * quarter) << 16) + half * (BN / 2);
     float *st = staging + ew * 32 * 32;
     const Epi &e = a.g.e;
+    float *sbias = reinterpret_cast<float *>(smem + RING + STAGING) + ew * 32;
+    // results that need nothing more are rounded before they are staged
+    const bool half_rows = e.mode == MODE_OUT && e.otype == E2F_BF16 && !e.extra;
     constexpr int NCH = BN / 64;   // 32-column chunks of this warp
     const int r8 = lane >> 2, cg = (lane & 3) * 8;
     int u = 0;
@@ -199,6 +207,30 @@ gemm_tma_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ 
     for (int i = blockIdx.x; i < a.tiles && ok; i += gridDim.x) {
       const Tile t = tile_of<BN>(a, i);
       const int nw = t.n0 + half * (BN / 2), mw = t.m0 + 32 * quarter;
+      auto load_extra = [&](Extra &d, int c) {   // 8 rows x 4 pieces of 8 columns an instruction
+        const int ng = nw + 32 * c + cg;
+        if (!a.vec || !e.extra || ng >= a.g.N) return;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int m = mw + 8 * q + r8;
+          if (m < a.g.M) {
+            const size_t o = (size_t)(m * e.lde) + ng;
+            if (e.etype == E2F_F32) {
+              const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const float *>(e.extra) + o);
+              d.lo[q] = p[0];
+              d.hi[q] = p[1];
+            } else {
+              d.lo[q] = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(e.extra) + o);
+            }
+          }
+        }
+      };
+      Extra x;
+      float bias = 0.f;
+      if (FULL_EPI) {
+        if (!LONGK) load_extra(x, 0);
+        if (e.bias && nw + lane < a.g.N) bias = __ldg(e.bias + nw + lane);
+      }
       float acc[LONGK ? BN / 2 : 1];
       if (LONGK) {
 #pragma unroll
@@ -227,70 +259,85 @@ gemm_tma_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ 
 #pragma unroll 1
       for (int c = 0; c < NCH; ++c) {
         const int n = nw + 32 * c;
-        if (n < a.g.N && mw < a.g.M) {
-          const bool part = !FULL_EPI && e.mode == MODE_PART;
-          const int ng = n + cg;
-          // what the epilogue reads, on its way while the accumulators move
-          uint4 x0[4], x1[4];
-          float bias = 0.f;
-          if (FULL_EPI) {
-            if (e.bias && n + lane < a.g.N) bias = __ldg(e.bias + n + lane);
-            if (a.vec && e.extra && ng < a.g.N) {
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                const int m = mw + 8 * q + r8;
-                if (m < a.g.M) {
-                  const size_t o = (size_t)(m * e.lde) + ng;
-                  if (e.etype == E2F_F32) {
-                    const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const float *>(e.extra) + o);
-                    x0[q] = p[0];
-                    x1[q] = p[1];
-                  } else {
-                    x0[q] = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(e.extra) + o);
-                  }
-                }
-              }
-            }
-          }
-          // lane = row: accumulators, bias, activation -> staging
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            float v[16];
-            if (LONGK) {
-#pragma unroll
-              for (int k = 0; k < NCH; ++k)
-                if (k == c) {
-#pragma unroll
-                  for (int j = 0; j < 16; ++j) v[j] = acc[LONGK ? 32 * k + 16 * h + j : 0];
-                }
-            } else {
-              tmem_ld_32x32b_x16(tq + (u & 1) * BN + 32 * c + 16 * h, v);
-            }
-            if (FULL_EPI) {
-#pragma unroll
-              for (int j = 0; j < 16; ++j) v[j] += __shfl_sync(0xffffffffu, bias, 16 * h + j);
-              if (e.mode == MODE_OUT) {
-                if (e.act == E2F_ACT_SILU) {
-#pragma unroll
-                  for (int j = 0; j < 16; ++j) v[j] = silu(v[j]);
-                } else if (e.act == E2F_ACT_GELU) {
-#pragma unroll
-                  for (int j = 0; j < 16; ++j) v[j] = gelu(v[j]);
-                }
-              } else if (e.act == E2F_ACT_SILU) {
-#pragma unroll
-                for (int j = 0; j < 16; ++j) v[j] = silu_grad(v[j]);
-              } else {
-#pragma unroll
-                for (int j = 0; j < 16; ++j) v[j] = gelu_grad(v[j]);
-              }
-            }
-#pragma unroll
-            for (int j = 0; j < 4; ++j)
-              *reinterpret_cast<float4 *>(st + lane * 32 + (((4 * h + j) ^ (lane & 7)) << 2)) =
-                  make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-          }
+        if (n >= a.g.N || mw >= a.g.M) break;
+        const int ng = n + cg;
+        const bool more = c + 1 < NCH && n + 32 < a.g.N;
+        Extra nx;
+        float nbias = 0.f;
+        if (FULL_EPI) {   // what the next chunk reads, on its way meanwhile
+          if (LONGK) load_extra(x, c);
+          else if (more) load_extra(nx, c + 1);
+          if (more && e.bias && n + 32 + lane < a.g.N) nbias = __ldg(e.bias + n + 32 + lane);
+          sbias[lane] = bias;
           __syncwarp();
+        }
+        // lane = row: accumulators, bias, activation
+        float v[32];
+        if (LONGK) {
+#pragma unroll
+          for (int k = 0; k < NCH; ++k)
+            if (k == c) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = acc[LONGK ? 32 * k + j : 0];
+            }
+        } else {
+          tmem_ld_32x32b_x32(tq + (u & 1) * BN + 32 * c, v);
+        }
+        if (FULL_EPI) {
+          if (e.bias) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+              const float4 b4 = *reinterpret_cast<const float4 *>(sbias + 4 * j);
+              v[4 * j] += b4.x; v[4 * j + 1] += b4.y; v[4 * j + 2] += b4.z; v[4 * j + 3] += b4.w;
+            }
+          }
+          if (e.mode == MODE_OUT) {
+            if (e.act == E2F_ACT_SILU) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = silu(v[j]);
+            } else if (e.act == E2F_ACT_GELU) {
+#pragma unroll
+              for (int j = 0; j < 32; ++j) v[j] = gelu(v[j]);
+            }
+          } else if (e.act == E2F_ACT_SILU) {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = silu_grad(v[j]);
+          } else {
+#pragma unroll
+            for (int j = 0; j < 32; ++j) v[j] = gelu_grad(v[j]);
+          }
+        }
+        if (half_rows) {
+          // bf16 results as they go out: half the shared-memory traffic
+          uint4 *sh = reinterpret_cast<uint4 *>(st);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            sh[lane * 4 + (j ^ ((lane >> 1) & 3))] =
+                make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
+                           pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
+          __syncwarp();
+          __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(e.out);
+          if (a.vec) {
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              const int row = 8 * q + r8, m = mw + row;
+              const uint4 w = sh[row * 4 + ((lane & 3) ^ ((row >> 1) & 3))];
+              if (m < a.g.M && ng < a.g.N) *reinterpret_cast<uint4 *>(out + (size_t)(m * e.ldo) + ng) = w;
+            }
+          } else if (n + lane < a.g.N) {
+            const __nv_bfloat16 *s2 = reinterpret_cast<const __nv_bfloat16 *>(st);
+#pragma unroll 8
+            for (int r = 0; r < 32; ++r)
+              if (mw + r < a.g.M)
+                out[(size_t)((mw + r) * e.ldo) + n + lane] = s2[r * 32 + (((lane >> 3) ^ ((r >> 1) & 3)) << 3) + (lane & 7)];
+          }
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j)
+            *reinterpret_cast<float4 *>(st + lane * 32 + ((j ^ (lane & 7)) << 2)) =
+                make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+          __syncwarp();
+          float *part = FULL_EPI || e.mode != MODE_PART ? nullptr : a.g.part + (size_t)t.split * a.g.M * a.g.N;
           if (a.vec) {
             float cs[8];
 #pragma unroll
@@ -300,29 +347,27 @@ gemm_tma_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ 
               const int row = 8 * q + r8, m = mw + row;
               if (m < a.g.M && ng < a.g.N) {
                 const float4 lo = *reinterpret_cast<const float4 *>(st + row * 32 + (((cg >> 2) ^ (row & 7)) << 2));
-                const float4 hi = *reinterpret_cast<const float4 *>(st + row * 32 + (((cg >> 2) + 1 ^ (row & 7)) << 2));
-                float v[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
+                const float4 hi = *reinterpret_cast<const float4 *>(st + row * 32 + ((((cg >> 2) + 1) ^ (row & 7)) << 2));
+                float r[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
                 if (part) {
-                  store8(a.g.part, E2F_F32, ((size_t)t.split * a.g.M + m) * a.g.N + ng, v);
-                } else if (!FULL_EPI) {
-                  store8(e.out, e.otype, (size_t)(m * e.ldo) + ng, v);
-                } else {
-                  float x[8];
-                  if (e.extra) unpack8(x0[q], x1[q], e.etype, x);
+                  store8(part, E2F_F32, (size_t)m * a.g.N + ng, r);
+                  continue;
+                }
+                if (FULL_EPI && e.extra) {
+                  float y[8];
+                  unpack8(x.lo[q], x.hi[q], e.etype, y);
                   if (e.mode == MODE_OUT) {
-                    if (e.extra) {
 #pragma unroll
-                      for (int j = 0; j < 8; ++j) v[j] += x[j];
-                    }
+                    for (int j = 0; j < 8; ++j) r[j] += y[j];
                   } else {
 #pragma unroll
                     for (int j = 0; j < 8; ++j) {
-                      v[j] *= x[j];
-                      cs[j] += v[j];
+                      r[j] *= y[j];
+                      cs[j] += r[j];
                     }
                   }
-                  if (e.out) store8(e.out, e.otype, (size_t)(m * e.ldo) + ng, v);
                 }
+                if (e.out) store8(e.out, e.otype, (size_t)(m * e.ldo) + ng, r);
               }
             }
             if (FULL_EPI && e.mode == MODE_DZ && e.colpart) {   // column sums of the warp's 32 rows
@@ -336,25 +381,36 @@ gemm_tma_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ 
           } else if (n + lane < a.g.N) {   // any alignment: lane = column
             const int nl = n + lane;
             float cs = 0.f;
-#pragma unroll 4
-            for (int r = 0; r < 32; ++r) {
-              const int m = mw + r;
-              if (m >= a.g.M) break;
-              float v = st[r * 32 + ((((lane >> 2) ^ (r & 7)) << 2) | (lane & 3))];
-              if (part) {
-                a.g.part[((size_t)t.split * a.g.M + m) * a.g.N + nl] = v;
-              } else {
-                if (FULL_EPI && e.extra) {
-                  const float x = load_as(e.extra, e.etype, (size_t)(m * e.lde) + nl);
-                  v = e.mode == MODE_OUT ? v + x : v * x;
-                  cs += v;
+            for (int r0 = 0; r0 < 32 && mw + r0 < a.g.M; r0 += 8) {
+              float y[8];
+              if (FULL_EPI && e.extra) {
+#pragma unroll
+                for (int r = 0; r < 8; ++r)
+                  y[r] = mw + r0 + r < a.g.M ? load_as(e.extra, e.etype, (size_t)((mw + r0 + r) * e.lde) + nl) : 0.f;
+              }
+#pragma unroll
+              for (int r = 0; r < 8; ++r) {
+                const int row = r0 + r, m = mw + row;
+                if (m >= a.g.M) break;
+                float w = st[row * 32 + ((((lane >> 2) ^ (row & 7)) << 2) | (lane & 3))];
+                if (part) {
+                  part[(size_t)m * a.g.N + nl] = w;
+                  continue;
                 }
-                if (e.out) store_as(e.out, e.otype, (size_t)(m * e.ldo) + nl, v);
+                if (FULL_EPI && e.extra) {
+                  w = e.mode == MODE_OUT ? w + y[r] : w * y[r];
+                  cs += w;
+                }
+                if (e.out) store_as(e.out, e.otype, (size_t)(m * e.ldo) + nl, w);
               }
             }
             if (FULL_EPI && e.mode == MODE_DZ && e.colpart) e.colpart[(size_t)(mw >> 5) * a.g.N + nl] = cs;
           }
-          __syncwarp();
+        }
+        __syncwarp();
+        if (FULL_EPI) {
+          if (!LONGK && more) x = nx;
+          bias = nbias;
         }
       }
       if (!LONGK) {
