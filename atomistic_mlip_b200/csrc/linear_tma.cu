@@ -26,15 +26,18 @@ namespace lin {
 namespace tma {
 
 constexpr int BM = 128, BK = 64;
-constexpr int NT = 320;
-constexpr int EPI_WARPS = 8;
+constexpr int SHORTK = 8;                        // blocks of 64: up to here 16 epilogue warps
 constexpr int KCHUNK = 16;                       // blocks of 64 per chain (LONGK)
-constexpr int STAGING = EPI_WARPS * 32 * 32 * 4;
-constexpr int SBIAS = EPI_WARPS * 32 * 4;
-constexpr int RING = 196608;
+
+// EW epilogue warps (8 or 16) beside warps 0 and 1; 16 take a quarter of the
+// columns each and leave less room for the ring.
+template <int EW> constexpr int threads() { return (EW == 16 ? 4 : 2) * 32 + EW * 32; }
+template <int EW> constexpr int staging() { return EW * 32 * 32 * 4; }
+template <int EW> constexpr int sbias() { return EW * 32 * 4; }
+template <int EW> constexpr int ring() { return EW == 16 ? 147456 : 196608; }
 template <int BN> constexpr int stage_bytes() { return (BM + BN) * BK * 2; }
-template <int BN> constexpr int stages() { return RING / stage_bytes<BN>(); }
-constexpr size_t SMEM = RING + STAGING + SBIAS + 256 + 1024;
+template <int BN, int EW> constexpr int stages() { return ring<EW>() / stage_bytes<BN>(); }
+template <int EW> constexpr size_t smem_bytes() { return ring<EW>() + staging<EW>() + sbias<EW>() + 256 + 1024; }
 
 struct Args {
   Gemm g;
@@ -115,14 +118,17 @@ __device__ __forceinline__ void store8(void *p, int type, size_t i, const float 
   }
 }
 
-// FULL_EPI: bias, activation, extra (MODE_OUT, MODE_DZ); else accumulators as
-// they are to out or to the partial sums.
-template <bool AMN, bool BMN, int BN, bool LONGK, bool FULL_EPI>
-__global__ void __launch_bounds__(NT, 1)
+// EPI: what the epilogue does.  PLAIN: accumulators as they are, to out or to
+// the partial sums; ACT: bias and activation; RES: those and the residual; DZ:
+// MODE_DZ.  (One instance for all of them kept the registers of the last two
+// alive in the others and spilled: 100,002 x 128 -> 512 with a bias 64 us.)
+constexpr int PLAIN = 0, ACT = 1, RES = 2, DZ = 3;
+template <bool AMN, bool BMN, int BN, bool LONGK, int EPI, int EW>
+__global__ void __launch_bounds__(threads<EW>(), 1)
 gemm_tma_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tbm,
                 const __grid_constant__ Args a) {
   using namespace tc;
-  constexpr int ST = stages<BN>(), SB = stage_bytes<BN>(), ABYTES = BM * BK * 2;
+  constexpr int ST = stages<BN, EW>(), RING = ring<EW>(), STAGING = staging<EW>(), SBIAS = sbias<EW>(), SB = stage_bytes<BN>(), ABYTES = BM * BK * 2;
   constexpr uint32_t LIMIT = 1u << 26;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -133,7 +139,7 @@ gemm_tma_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < ST; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
-    for (int i = 0; i < 2; ++i) { mbar_init(&tfull[i], 1); mbar_init(&tempty[i], EPI_WARPS); }
+    for (int i = 0; i < 2; ++i) { mbar_init(&tfull[i], 1); mbar_init(&tempty[i], EW); }
     mbar_fence_init();
   }
   __syncthreads();
@@ -192,29 +198,35 @@ gemm_tma_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ 
       }
       if (!ok) atomicExch(a.err, E2F_ERR_TIMEOUT);
     }
-  } else {
-    const int ew = warp - 2, quarter = warp & 3, half = ew >> 2;   // TMEM lanes 32 quarter + .., columns half * BN / 2 + ..
-    const uint32_t tq = tmem + ((uint32_t)(32 * quarter) << 16) + half * (BN / 2);
+  } else if (warp < 2 + EW) {
+    constexpr int BW = BN * 4 / EW;                              // columns of this warp
+    const int ew = warp - 2, quarter = warp & 3, cols = (ew >> 2) * BW;   // TMEM lanes 32 quarter + ..
+    const uint32_t tq = tmem + ((uint32_t)(32 * quarter) << 16) + cols;
     float *st = staging + ew * 32 * 32;
     const Epi &e = a.g.e;
     float *sbias = reinterpret_cast<float *>(smem + RING + STAGING) + ew * 32;
     // results that need nothing more are rounded before they are staged
-    const bool half_rows = e.mode == MODE_OUT && e.otype == E2F_BF16 && !e.extra;
-    constexpr int NCH = BN / 64;   // 32-column chunks of this warp
+    const bool half_rows = EPI <= ACT && e.mode == MODE_OUT && e.otype == E2F_BF16;
+    constexpr int NCH = BW / 32;   // 32-column chunks of this warp
     const int r8 = lane >> 2, cg = (lane & 3) * 8;
-    int u = 0;
+    int u = 0, bias_of = -1;
+    float bias[NCH];
     bool ok = true;
     for (int i = blockIdx.x; i < a.tiles && ok; i += gridDim.x) {
       const Tile t = tile_of<BN>(a, i);
-      const int nw = t.n0 + half * (BN / 2), mw = t.m0 + 32 * quarter;
+      const int nw = t.n0 + cols, mw = t.m0 + 32 * quarter;
+      // this lane's rows r8 + 8 q of the tile, by offset and step
+      const int rows = a.g.M - mw;
+      const long long ldo = e.mode == MODE_PART ? a.g.N : e.ldo;
+      const size_t ooff = (size_t)((long long)(mw + r8) * ldo), xoff = (size_t)((long long)(mw + r8) * e.lde);
+      const long long ostep = 8 * ldo, xstep = 8 * e.lde;
       auto load_extra = [&](Extra &d, int c) {   // 8 rows x 4 pieces of 8 columns an instruction
         const int ng = nw + 32 * c + cg;
         if (!a.vec || !e.extra || ng >= a.g.N) return;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const int m = mw + 8 * q + r8;
-          if (m < a.g.M) {
-            const size_t o = (size_t)(m * e.lde) + ng;
+          if (8 * q + r8 < rows) {
+            const size_t o = xoff + (size_t)(q * xstep) + ng;
             if (e.etype == E2F_F32) {
               const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const float *>(e.extra) + o);
               d.lo[q] = p[0];
@@ -225,22 +237,25 @@ gemm_tma_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ 
           }
         }
       };
-      Extra x;
-      float bias = 0.f;
-      if (FULL_EPI) {
-        if (!LONGK) load_extra(x, 0);
-        if (e.bias && nw + lane < a.g.N) bias = __ldg(e.bias + nw + lane);
+      if (EPI != PLAIN && nw != bias_of) {   // a CTA's tiles mostly share their columns
+        bias_of = nw;
+#pragma unroll
+        for (int k = 0; k < NCH; ++k)
+          bias[k] = e.bias && nw + 32 * k + lane < a.g.N ? __ldg(e.bias + nw + 32 * k + lane) : 0.f;
       }
-      float acc[LONGK ? BN / 2 : 1];
+      constexpr bool EXTRA = EPI >= RES, AHEAD = EXTRA && !LONGK && EW == 8;   // registers for the next chunk's extra
+      Extra x;
+      if (AHEAD) load_extra(x, 0);
+      float acc[LONGK ? BW : 1];
       if (LONGK) {
 #pragma unroll
-        for (int j = 0; j < BN / 2; ++j) acc[j] = 0.f;
+        for (int j = 0; j < BW; ++j) acc[j] = 0.f;
         for (int kc = t.kb0; kc < t.kb1; kc += KCHUNK, ++u) {
           ok = __all_sync(0xffffffffu, mbar_wait(&tfull[u & 1], (u >> 1) & 1, LIMIT));
           if (!ok) break;
           tc_fence_after();
 #pragma unroll
-          for (int c = 0; c < BN / 2; c += 16) {
+          for (int c = 0; c < BW; c += 16) {
             float v[16];
             tmem_ld_32x32b_x16(tq + (u & 1) * BN + c, v);
 #pragma unroll
@@ -263,66 +278,82 @@ gemm_tma_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ 
         const int ng = n + cg;
         const bool more = c + 1 < NCH && n + 32 < a.g.N;
         Extra nx;
-        float nbias = 0.f;
-        if (FULL_EPI) {   // what the next chunk reads, on its way meanwhile
-          if (LONGK) load_extra(x, c);
+        if (EXTRA) {   // what the epilogue reads, on its way while the accumulators move
+          if (!AHEAD) load_extra(x, c);
           else if (more) load_extra(nx, c + 1);
-          if (more && e.bias && n + 32 + lane < a.g.N) nbias = __ldg(e.bias + n + 32 + lane);
-          sbias[lane] = bias;
+        }
+        if (EPI != PLAIN) {
+          float b = bias[0];
+#pragma unroll
+          for (int k = 1; k < NCH; ++k) b = k == c ? bias[k] : b;
+          sbias[lane] = b;
           __syncwarp();
         }
-        // lane = row: accumulators, bias, activation
-        float v[32];
-        if (LONGK) {
+        // lane = row: accumulators, bias, activation -> staging, PW columns at a
+        // time (16 where the extra's registers live beside them)
+        constexpr int PW = EXTRA && EW == 16 ? 16 : 32;
+        uint4 *sh = reinterpret_cast<uint4 *>(st);
 #pragma unroll
-          for (int k = 0; k < NCH; ++k)
-            if (k == c) {
+        for (int h = 0; h < 32 / PW; ++h) {
+          float v[PW];
+          if constexpr (LONGK) {
 #pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] = acc[LONGK ? 32 * k + j : 0];
+            for (int k = 0; k < NCH; ++k)
+              if (k == c) {
+#pragma unroll
+                for (int j = 0; j < PW; ++j) v[j] = acc[32 * k + PW * h + j];
+              }
+          } else if constexpr (PW == 32) {
+            tmem_ld_32x32b_x32(tq + (u & 1) * BN + 32 * c, v);
+          } else {
+            tmem_ld_32x32b_x16(tq + (u & 1) * BN + 32 * c + PW * h, v);
+          }
+          if (EPI != PLAIN) {
+            if (e.bias) {
+#pragma unroll
+              for (int j = 0; j < PW / 4; ++j) {
+                const float4 b4 = *reinterpret_cast<const float4 *>(sbias + PW * h + 4 * j);
+                v[4 * j] += b4.x; v[4 * j + 1] += b4.y; v[4 * j + 2] += b4.z; v[4 * j + 3] += b4.w;
+              }
             }
-        } else {
-          tmem_ld_32x32b_x32(tq + (u & 1) * BN + 32 * c, v);
-        }
-        if (FULL_EPI) {
-          if (e.bias) {
+            if (EPI != DZ) {
+              if (e.act == E2F_ACT_SILU) {
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
-              const float4 b4 = *reinterpret_cast<const float4 *>(sbias + 4 * j);
-              v[4 * j] += b4.x; v[4 * j + 1] += b4.y; v[4 * j + 2] += b4.z; v[4 * j + 3] += b4.w;
+                for (int j = 0; j < PW; ++j) v[j] = silu(v[j]);
+              } else if (e.act == E2F_ACT_GELU) {
+#pragma unroll
+                for (int j = 0; j < PW; ++j) v[j] = gelu(v[j]);
+              }
+            } else if (e.act == E2F_ACT_SILU) {
+#pragma unroll
+              for (int j = 0; j < PW; ++j) v[j] = silu_grad(v[j]);
+            } else {
+#pragma unroll
+              for (int j = 0; j < PW; ++j) v[j] = gelu_grad(v[j]);
             }
           }
-          if (e.mode == MODE_OUT) {
-            if (e.act == E2F_ACT_SILU) {
+          if (half_rows) {   // bf16 results as they go out: half the shared-memory traffic
 #pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] = silu(v[j]);
-            } else if (e.act == E2F_ACT_GELU) {
-#pragma unroll
-              for (int j = 0; j < 32; ++j) v[j] = gelu(v[j]);
-            }
-          } else if (e.act == E2F_ACT_SILU) {
-#pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = silu_grad(v[j]);
+            for (int j = 0; j < PW / 8; ++j)
+              sh[lane * 4 + ((PW / 8 * h + j) ^ ((lane >> 1) & 3))] =
+                  make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
+                             pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
           } else {
 #pragma unroll
-            for (int j = 0; j < 32; ++j) v[j] = gelu_grad(v[j]);
+            for (int j = 0; j < PW / 4; ++j)
+              *reinterpret_cast<float4 *>(st + lane * 32 + (((PW / 4 * h + j) ^ (lane & 7)) << 2)) =
+                  make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
           }
         }
+        __syncwarp();
         if (half_rows) {
-          // bf16 results as they go out: half the shared-memory traffic
-          uint4 *sh = reinterpret_cast<uint4 *>(st);
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            sh[lane * 4 + (j ^ ((lane >> 1) & 3))] =
-                make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
-                           pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
-          __syncwarp();
           __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(e.out);
           if (a.vec) {
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              const int row = 8 * q + r8, m = mw + row;
+              const int row = 8 * q + r8;
               const uint4 w = sh[row * 4 + ((lane & 3) ^ ((row >> 1) & 3))];
-              if (m < a.g.M && ng < a.g.N) *reinterpret_cast<uint4 *>(out + (size_t)(m * e.ldo) + ng) = w;
+              if (row < rows && ng < a.g.N) *reinterpret_cast<uint4 *>(out + ooff + (size_t)(q * ostep) + ng) = w;
             }
           } else if (n + lane < a.g.N) {
             const __nv_bfloat16 *s2 = reinterpret_cast<const __nv_bfloat16 *>(st);
@@ -332,31 +363,26 @@ gemm_tma_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ 
                 out[(size_t)((mw + r) * e.ldo) + n + lane] = s2[r * 32 + (((lane >> 3) ^ ((r >> 1) & 3)) << 3) + (lane & 7)];
           }
         } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j)
-            *reinterpret_cast<float4 *>(st + lane * 32 + ((j ^ (lane & 7)) << 2)) =
-                make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
-          __syncwarp();
-          float *part = FULL_EPI || e.mode != MODE_PART ? nullptr : a.g.part + (size_t)t.split * a.g.M * a.g.N;
+          float *part = EPI != PLAIN || e.mode != MODE_PART ? nullptr : a.g.part + (size_t)t.split * a.g.M * a.g.N;
           if (a.vec) {
             float cs[8];
 #pragma unroll
             for (int j = 0; j < 8; ++j) cs[j] = 0.f;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
-              const int row = 8 * q + r8, m = mw + row;
-              if (m < a.g.M && ng < a.g.N) {
+              const int row = 8 * q + r8;
+              if (row < rows && ng < a.g.N) {
                 const float4 lo = *reinterpret_cast<const float4 *>(st + row * 32 + (((cg >> 2) ^ (row & 7)) << 2));
                 const float4 hi = *reinterpret_cast<const float4 *>(st + row * 32 + ((((cg >> 2) + 1) ^ (row & 7)) << 2));
                 float r[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
                 if (part) {
-                  store8(part, E2F_F32, (size_t)m * a.g.N + ng, r);
+                  store8(part, E2F_F32, ooff + (size_t)(q * ostep) + ng, r);
                   continue;
                 }
-                if (FULL_EPI && e.extra) {
+                if (EXTRA) {
                   float y[8];
                   unpack8(x.lo[q], x.hi[q], e.etype, y);
-                  if (e.mode == MODE_OUT) {
+                  if (EPI == RES) {
 #pragma unroll
                     for (int j = 0; j < 8; ++j) r[j] += y[j];
                   } else {
@@ -367,10 +393,10 @@ gemm_tma_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ 
                     }
                   }
                 }
-                if (e.out) store8(e.out, e.otype, (size_t)(m * e.ldo) + ng, r);
+                if (EPI != DZ || e.out) store8(e.out, e.otype, ooff + (size_t)(q * ostep) + ng, r);
               }
             }
-            if (FULL_EPI && e.mode == MODE_DZ && e.colpart) {   // column sums of the warp's 32 rows
+            if (EPI == DZ && e.colpart) {   // column sums of the warp's 32 rows
 #pragma unroll
               for (int j = 0; j < 8; ++j) {
 #pragma unroll
@@ -383,7 +409,7 @@ gemm_tma_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ 
             float cs = 0.f;
             for (int r0 = 0; r0 < 32 && mw + r0 < a.g.M; r0 += 8) {
               float y[8];
-              if (FULL_EPI && e.extra) {
+              if (EXTRA) {
 #pragma unroll
                 for (int r = 0; r < 8; ++r)
                   y[r] = mw + r0 + r < a.g.M ? load_as(e.extra, e.etype, (size_t)((mw + r0 + r) * e.lde) + nl) : 0.f;
@@ -397,21 +423,18 @@ gemm_tma_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ 
                   part[(size_t)m * a.g.N + nl] = w;
                   continue;
                 }
-                if (FULL_EPI && e.extra) {
-                  w = e.mode == MODE_OUT ? w + y[r] : w * y[r];
+                if (EXTRA) {
+                  w = EPI == RES ? w + y[r] : w * y[r];
                   cs += w;
                 }
-                if (e.out) store_as(e.out, e.otype, (size_t)(m * e.ldo) + nl, w);
+                if (EPI != DZ || e.out) store_as(e.out, e.otype, (size_t)(m * e.ldo) + nl, w);
               }
             }
-            if (FULL_EPI && e.mode == MODE_DZ && e.colpart) e.colpart[(size_t)(mw >> 5) * a.g.N + nl] = cs;
+            if (EPI == DZ && e.colpart) e.colpart[(size_t)(mw >> 5) * a.g.N + nl] = cs;
           }
         }
         __syncwarp();
-        if (FULL_EPI) {
-          if (!LONGK && more) x = nx;
-          bias = nbias;
-        }
+        if (AHEAD && more) x = nx;
       }
       if (!LONGK) {
         tc_fence_before();
@@ -457,20 +480,30 @@ static bool encode(CUtensorMap *m, const void *p, long long rows, long long cols
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool AMN, bool BMN, int BN, bool LONGK, bool FULL_EPI>
+template <bool AMN, bool BMN, int BN, bool LONGK, int EPI, int EW>
 static e2f_status launch_epi(const CUtensorMap &ta, const CUtensorMap &tb, const Args &a, int sms, cudaStream_t s) {
-  auto k = gemm_tma_kernel<AMN, BMN, BN, LONGK, FULL_EPI>;
-  E2F_CUDA_TRY(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)SMEM));
-  E2F_LAUNCH(k, std::min(a.tiles, sms), NT, SMEM, s, ta, tb, a);
+  auto k = gemm_tma_kernel<AMN, BMN, BN, LONGK, EPI, EW>;
+  E2F_CUDA_TRY(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<EW>()));
+  E2F_LAUNCH(k, std::min(a.tiles, sms), threads<EW>(), smem_bytes<EW>(), s, ta, tb, a);
   return E2F_OK;
 }
 
 template <bool AMN, bool BMN, int BN, bool LONGK>
 static e2f_status launch(const CUtensorMap &ta, const CUtensorMap &tb, const Args &a, int sms, cudaStream_t s) {
   const Epi &e = a.g.e;
-  if (!AMN && !BMN && e.mode != MODE_PART && (e.mode == MODE_DZ || e.bias || e.extra || e.act != E2F_ACT_NONE))
-    return launch_epi<AMN, BMN, BN, LONGK, !AMN && !BMN>(ta, tb, a, sms, s);
-  return launch_epi<AMN, BMN, BN, LONGK, false>(ta, tb, a, sms, s);
+  // A short contraction leaves the epilogue as the longer part of a tile.
+  constexpr int W = LONGK ? 8 : 16;
+  const bool wide = !LONGK && a.g.kper <= SHORTK;
+#define E2F_LIN_EPI(E)                                                                \
+  return wide ? launch_epi<AMN, BMN, BN, LONGK, E, W>(ta, tb, a, sms, s)              \
+              : launch_epi<AMN, BMN, BN, LONGK, E, 8>(ta, tb, a, sms, s)
+  if constexpr (!AMN && !BMN) {
+    if (e.mode == MODE_DZ) E2F_LIN_EPI(DZ);
+    if (e.mode == MODE_OUT && e.extra) E2F_LIN_EPI(RES);
+    if (e.mode == MODE_OUT && (e.bias || e.act != E2F_ACT_NONE)) E2F_LIN_EPI(ACT);
+  }
+  E2F_LIN_EPI(PLAIN);
+#undef E2F_LIN_EPI
 }
 
 }  // namespace tma
