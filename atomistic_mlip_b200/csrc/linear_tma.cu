@@ -4,7 +4,7 @@
 // A persistent CTA per SM walks output tiles of 128 x BN (BN = 128 or 256).
 // Warp 0 loads 64-wide operand slices by TMA into a ring of stages (128-byte
 // swizzle; rows and columns outside the matrices arrive as zeros), warp 1
-// issues the MMAs into one of two accumulators in tensor memory, warps 2-9
+// issues the MMAs into one of two accumulators in tensor memory, warps 4 on
 // run the epilogue of the other one meanwhile: TMEM -> shared memory -> rows,
 // so that residual, dL/dout and results move in 16-byte pieces of contiguous
 // rows.
@@ -29,9 +29,9 @@ constexpr int BM = 128, BK = 64;
 constexpr int SHORTK = 8;                        // blocks of 64: up to here 16 epilogue warps
 constexpr int KCHUNK = 16;                       // blocks of 64 per chain (LONGK)
 
-// EW epilogue warps (8 or 16) beside warps 0 and 1; 16 take a quarter of the
+// EW epilogue warps (8 or 16) behind the four of the control warpgroup; 16 take a quarter of the
 // columns each and leave less room for the ring.
-template <int EW> constexpr int threads() { return (EW == 16 ? 4 : 2) * 32 + EW * 32; }
+template <int EW> constexpr int threads() { return (4 + EW) * 32; }
 template <int EW> constexpr int staging() { return EW * 32 * 32 * 4; }
 template <int EW> constexpr int sbias() { return EW * 32 * 4; }
 template <int EW> constexpr int ring() { return EW == 16 ? 147456 : 196608; }
@@ -149,6 +149,9 @@ gemm_tma_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ 
   tc_fence_after();
   const uint32_t tmem = tslot;
 
+  // LONGK: the register sums need more than the 168 that 384 threads are
+  // launched with: 40 + 2 * 232 = 3 * 168.
+  if (LONGK && warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
   if (warp == 0) {
     if (lane == 0) {
       int s = 0;
@@ -198,9 +201,10 @@ gemm_tma_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ 
       }
       if (!ok) atomicExch(a.err, E2F_ERR_TIMEOUT);
     }
-  } else if (warp < 2 + EW) {
+  } else if (warp >= 4) {
+    if (LONGK) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
     constexpr int BW = BN * 4 / EW;                              // columns of this warp
-    const int ew = warp - 2, quarter = warp & 3, cols = (ew >> 2) * BW;   // TMEM lanes 32 quarter + ..
+    const int ew = warp - 4, quarter = warp & 3, cols = (ew >> 2) * BW;   // TMEM lanes 32 quarter + ..
     const uint32_t tq = tmem + ((uint32_t)(32 * quarter) << 16) + cols;
     float *st = staging + ew * 32 * 32;
     const Epi &e = a.g.e;
