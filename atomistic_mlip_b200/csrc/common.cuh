@@ -39,6 +39,47 @@ int *device_error_flag();   // per-device int latched by kernels, or nullptr
     }                                                                      \
   } while (0)
 
+// Launch behind another kernel of the same call: it may start while that one
+// drains, and must wait for it (griddepcontrol.wait) before it touches memory.
+template <typename... P, typename... A>
+inline cudaError_t launch_after(void (*k)(P...), dim3 grid, dim3 block, size_t smem, cudaStream_t s, A... args) {
+  cudaLaunchConfig_t c{};
+  cudaLaunchAttribute at{};
+  at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at.val.programmaticStreamSerializationAllowed = 1;
+  c.gridDim = grid;
+  c.blockDim = block;
+  c.dynamicSmemBytes = smem;
+  c.stream = s;
+  c.attrs = &at;
+  c.numAttrs = 1;
+  return cudaLaunchKernelEx(&c, k, static_cast<P>(args)...);
+}
+#define E2F_LAUNCH_AFTER(kernel, grid, block, smem, stream, ...)                          \
+  do {                                                                                    \
+    const cudaError_t e2f_lerr_ =                                                         \
+        ::e2f::launch_after(kernel, dim3(grid), dim3(block), (smem), (stream), __VA_ARGS__); \
+    ::e2f::g_launches.fetch_add(1, std::memory_order_relaxed);                            \
+    if (e2f_lerr_ != cudaSuccess) {                                                       \
+      ::e2f::set_cuda_error(e2f_lerr_, "launch of " #kernel);                             \
+      return E2F_ERR_CUDA;                                                                \
+    }                                                                                     \
+  } while (0)
+
+// Dynamic shared memory of kernel K (always the same size), allowed once per
+// device: the attribute call costs as much host time as a quarter of a launch.
+template <auto K> cudaError_t allow_smem(size_t bytes) {
+  static std::atomic<uint64_t> done{0};
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
+  if (e != cudaSuccess) return e;
+  const uint64_t bit = 1ull << (dev & 63);
+  if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  e = cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+  if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
+  return e;
+}
+
 // Stream-ordered scratch buffer released (in stream order) on scope exit.
 struct Scratch {
   void *p = nullptr;

@@ -18,9 +18,11 @@
 //   reduce_kernel    a CTA per tile of the sorted order; a row group per
 //                    contiguous piece of the tile; sums of runs that end
 //                    inside are written, the open ends (at most one at the
-//                    head and one at the tail) are kept as partial rows.
-//                    Further CTAs write zeros to the ids that do not occur.
+//                    head and one at the tail) are kept as partial rows
 //   combine_kernel   runs over several tiles: their partial rows in order
+// The sort is bound by latency and leaves the memory idle: the table is zeroed
+// meanwhile, by further CTAs of its kernels.  Up to SMALL_N rows one kernel does
+// it all: a CTA sorts the rows of its own few ids in shared memory.
 // Every sum has a fixed order: the result repeats bit for bit.
 #include <algorithm>
 
@@ -30,6 +32,12 @@ namespace e2f {
 namespace emb {
 
 constexpr int NT = 256;
+
+// The kernels of one call start while the one before drains (programmatic
+// dependent launch) and wait here before they read what it wrote.
+__device__ __forceinline__ void after_previous() {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+}
 
 // VE consecutive elements of a row as floats (VE * sizeof(T) is 16, 4 or the
 // element's size; the caller guarantees that alignment).
@@ -95,15 +103,16 @@ template <> struct Vec<__nv_bfloat16, 1> {
 // lookup
 // ---------------------------------------------------------------------------
 // The output is one flat run of N * VR vectors of VE elements, VR = Q D / VE;
-// a CTA takes FWD_U * NT consecutive ones, so every store instruction of a
+// a CTA takes fwd_u * NT consecutive ones, so every store instruction of a
 // warp is one contiguous piece.  The vector's row and place in the row advance
 // by the (quotient, remainder) of NT by VR: no division per vector.
-constexpr int FWD_U = 4;
+template <int VE, typename O> constexpr int fwd_u() { return VE * sizeof(O) >= 8 ? 4 : 8; }   // vectors a thread
 
 template <typename I, typename T, typename O, int VE>
 __global__ void __launch_bounds__(NT) embed_fwd_kernel(const I *__restrict__ ids, long long nvec, int VR, int DV,
                                                        const T *__restrict__ table, long long V, float scale,
                                                        O *__restrict__ out, int *err) {
+  constexpr int FWD_U = fwd_u<VE, O>();
   const long long base = (long long)blockIdx.x * (FWD_U * NT);
   const long long r0 = base / VR;
   const unsigned t = (unsigned)(base - r0 * VR) + threadIdx.x;   // place counted from row r0
@@ -146,7 +155,8 @@ static e2f_status launch_fwd(const I *ids, int64_t N, const T *table, int64_t V,
   if (!err) return E2F_ERR_CUDA;
   const int DV = D / VE, VR = (int)((long long)Q * DV);
   const long long nvec = (long long)N * VR;
-  const long long grid = (nvec + FWD_U * NT - 1) / (FWD_U * NT);
+  constexpr int per = fwd_u<VE, O>() * NT;
+  const long long grid = (nvec + per - 1) / per;
   if (grid > INT32_MAX) return E2F_ERR_UNSUPPORTED;
   E2F_LAUNCH((embed_fwd_kernel<I, T, O, VE>), (unsigned)grid, NT, 0, s, ids, nvec, VR, DV, table, (long long)V, scale,
              out, err);
@@ -176,7 +186,23 @@ constexpr int MAX_TILES = 128;   // CTAs of a pass; longer inputs give each more
 struct SortArgs {
   int N, shift, tile;            // tile: keys per CTA, a multiple of SUB
   int V;
+  int tiles;                     // CTAs behind these write zeros to [z0, z1)
+  float *z0, *z1;
 };
+
+// The CTAs from `first` on write zeros to [a.z0, a.z1).
+__device__ __forceinline__ void zero_part(const SortArgs &a, int first) {
+  const size_t n = a.z1 - a.z0, ctas = gridDim.x - first, b = blockIdx.x - first;
+  const size_t per = ((n + ctas - 1) / ctas + 3) & ~(size_t)3;
+  float *p = a.z0 + min(n, b * per), *e = a.z0 + min(n, (b + 1) * per);
+  while (p < e && (reinterpret_cast<uintptr_t>(p) & 15)) {
+    if (threadIdx.x == 0) *p = 0.f;
+    ++p;
+  }
+  const size_t q = (e - p) >> 2;
+  for (size_t i = threadIdx.x; i < q; i += NT) reinterpret_cast<float4 *>(p)[i] = make_float4(0.f, 0.f, 0.f, 0.f);
+  if (p + 4 * q + threadIdx.x < e) p[4 * q + threadIdx.x] = 0.f;
+}
 
 // Key of a row: its id, or V (behind every id) for rows that take no part.
 template <typename I> __device__ __forceinline__ uint32_t key_of(const I *ids, int n, int V) {
@@ -189,6 +215,11 @@ template <typename I, bool FIRST>
 __global__ void __launch_bounds__(NT) hist_kernel(SortArgs a, const I *__restrict__ ids,
                                                   const uint32_t *__restrict__ keys, int *__restrict__ hist, int *err) {
   __shared__ int h[RB];
+  after_previous();
+  if ((int)blockIdx.x >= a.tiles) {
+    zero_part(a, a.tiles);
+    return;
+  }
   h[threadIdx.x] = 0;
   __syncthreads();
   const long long lo = (long long)blockIdx.x * a.tile;
@@ -217,10 +248,16 @@ __global__ void __launch_bounds__(NT) scatter_kernel(SortArgs a, const I *__rest
   __shared__ int scan[RB];
   __shared__ int base[RB];
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  after_previous();
+  if ((int)blockIdx.x >= a.tiles) {
+    zero_part(a, a.tiles);
+    return;
+  }
   // base[d]: keys of smaller digits anywhere, and of digit d in earlier tiles
   {
     int before = 0, total = 0;
-    for (int b = 0; b < (int)gridDim.x; ++b) {
+#pragma unroll 8
+    for (int b = 0; b < a.tiles; ++b) {
       const int c = hist[b * RB + t];
       if (b < (int)blockIdx.x) before += c;
       total += c;
@@ -294,6 +331,7 @@ struct RedArgs {
   long long ld;           // elements between rows of grad_out
   float scale;
   int accumulate;
+  bool gvec;              // rows of grad start on 16-byte boundaries
   const uint32_t *keys;   // sorted
   const int *rows;
   float *grad;            // [V][D]
@@ -301,50 +339,33 @@ struct RedArgs {
   int tiles;
 };
 
+// VE floats to p: 16 bytes at a time where the row starts on such a boundary.
+template <int VE> __device__ __forceinline__ void put_row(float *p, const float (&v)[VE], bool vec) {
+  if (VE >= 4 && vec) {
+#pragma unroll
+    for (int k = 0; k < VE / 4; ++k)
+      reinterpret_cast<float4 *>(p)[k] = make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < VE; ++k) p[k] = v[k];
+  }
+}
+// The sum of an id's rows (columns col .. col + VE, all inside: VE divides D).
 template <int VE> __device__ __forceinline__ void write_sum(const RedArgs &a, uint32_t key, int col, const float (&acc)[VE]) {
   float *p = a.grad + (size_t)key * a.D + col;
+  float v[VE];
 #pragma unroll
-  for (int k = 0; k < VE; ++k)
-    if (col + k < a.D) p[k] = a.accumulate ? p[k] + a.scale * acc[k] : a.scale * acc[k];
+  for (int k = 0; k < VE; ++k) v[k] = a.accumulate ? p[k] + a.scale * acc[k] : a.scale * acc[k];
+  put_row<VE>(p, v, a.gvec);
 }
 
-constexpr int ZROWS = 32;   // ids a zero-writing CTA looks after
-
+// Resident CTAs: the tile is chosen so that one wave of them covers the rows.
+constexpr int RED_CTAS = 4;
 template <typename T, int VE>
-__global__ void __launch_bounds__(NT) reduce_kernel(RedArgs a, const T *__restrict__ g) {
+__global__ void __launch_bounds__(NT, RED_CTAS) reduce_kernel(RedArgs a, const T *__restrict__ g) {
   extern __shared__ int sm[];
   const int t = threadIdx.x;
-  if ((int)blockIdx.x >= a.tiles) {
-    // ids v0 .. v0 + ZROWS that do not occur: zeros (first column block only
-    // launches these CTAs with blockIdx.y == 0 doing the whole row)
-    if (blockIdx.y != 0) return;
-    const long long v0 = (long long)((int)blockIdx.x - a.tiles) * ZROWS;
-    if (t < ZROWS) {
-      int absent = 0;
-      if (v0 + t < a.V) {
-        const uint32_t v = (uint32_t)(v0 + t);
-        int lo = 0, hi = a.N;   // first place with key >= v
-        while (lo < hi) {
-          const int mid = lo + ((hi - lo) >> 1);
-          if (a.keys[mid] < v) lo = mid + 1;
-          else hi = mid;
-        }
-        absent = lo == a.N || a.keys[lo] != v;
-      }
-      sm[t] = absent;
-    }
-    __syncthreads();
-    for (int r = 0; r < ZROWS; ++r)
-      if (sm[r]) {
-        float *p = a.grad + (size_t)(v0 + r) * a.D;
-        if ((a.D & 3) == 0 && (reinterpret_cast<uintptr_t>(a.grad) & 15) == 0) {
-          for (int c = t; c < a.D / 4; c += NT) reinterpret_cast<float4 *>(p)[c] = make_float4(0.f, 0.f, 0.f, 0.f);
-        } else {
-          for (int c = t; c < a.D; c += NT) p[c] = 0.f;
-        }
-      }
-    return;
-  }
+  after_previous();
   const int CL = a.CL, RG = NT / CL, R = a.R, G = R / RG;
   uint32_t *skey = reinterpret_cast<uint32_t *>(sm);      // [R + 2]: key before, the tile's, key behind
   int *srow = sm + R + 2;                                 // [R]
@@ -373,9 +394,20 @@ __global__ void __launch_bounds__(NT) reduce_kernel(RedArgs a, const T *__restri
     bool fresh = false;    // the open run started inside this group
     int flag = 0;          // 1: head partial, 2: it runs through the group, 4: tail partial
     if (i0 < i1) fresh = key[i0] != key[i0 - 1];
-    constexpr int U = 8;
+    constexpr int U = VE == 8 ? 4 : 8;   // rows in flight
     for (int i = i0; i < i1; i += U) {
       float v[U][VE];
+      if (i + U <= i1 && key[i] == key[i + U]) {   // sorted: all of them inside one run that goes on
+        if (in && key[i] < (uint32_t)a.V) {
+#pragma unroll
+          for (int u = 0; u < U; ++u) Vec<T, VE>::load(g + (size_t)srow[i + u] * a.ld + col, v[u]);
+#pragma unroll
+          for (int u = 0; u < U; ++u)
+#pragma unroll
+            for (int k = 0; k < VE; ++k) acc[k] += v[u][k];
+        }
+        continue;
+      }
 #pragma unroll
       for (int u = 0; u < U; ++u) {
 #pragma unroll
@@ -429,9 +461,7 @@ __global__ void __launch_bounds__(NT) reduce_kernel(RedArgs a, const T *__restri
         if (!(f & 2)) {   // ends in this group
           const uint32_t kk = key[q * G];
           if (!fresh) {
-#pragma unroll
-            for (int k = 0; k < VE; ++k)
-              if (col + k < a.D) a.head[(size_t)blockIdx.x * a.D + col + k] = acc[k];
+            put_row<VE>(a.head + (size_t)blockIdx.x * a.D + col, acc, true);
           } else if (kk < (uint32_t)a.V) {
             write_sum<VE>(a, kk, col, acc);
           }
@@ -445,52 +475,87 @@ __global__ void __launch_bounds__(NT) reduce_kernel(RedArgs a, const T *__restri
         open = fresh = true;
       }
       if (i1 == n && open) {   // runs on into the next tile
-        float *dst = fresh ? a.tail : a.head;
-#pragma unroll
-        for (int k = 0; k < VE; ++k)
-          if (col + k < a.D) dst[(size_t)blockIdx.x * a.D + col + k] = acc[k];
+        put_row<VE>((fresh ? a.tail : a.head) + (size_t)blockIdx.x * a.D + col, acc, true);
       }
     }
   }
 }
 
-// Runs over several tiles.  CTA (tile, column block) acts where a run starts
-// inside the tile and goes on behind it: its tail row, then the head rows of
-// the tiles up to the one where the run ends, JG of them side by side.
-constexpr int JG = 8;
+// Runs over several tiles.  A warp looks at one tile: where a run starts inside
+// the tile and goes on behind it, it adds the tail row and the head rows of the
+// tiles up to the one where the run ends.  Runs over more than 32 tiles are left
+// to the whole CTA, JG head rows side by side.
+constexpr int JG = 32;
 __global__ void __launch_bounds__(32 * JG) combine_kernel(RedArgs a) {
   __shared__ float part[JG][32];
-  const int lane = threadIdx.x & 31, jg = threadIdx.x >> 5;
-  const long long pe = ((long long)blockIdx.x + 1) * a.R;   // first place behind the tile
-  const uint32_t kk = a.keys[pe - 1];
-  if (a.keys[pe] != kk || kk >= (uint32_t)a.V) return;
-  const long long p0 = pe - a.R;
-  if (p0 > 0 && a.keys[p0 - 1] == kk) return;               // it started before this tile
-  long long lo = pe, hi = a.N;                              // first place behind the run
-  while (lo < hi) {
-    const long long mid = lo + ((hi - lo) >> 1);
-    if (a.keys[mid] <= kk) lo = mid + 1;
-    else hi = mid;
+  __shared__ int todo[JG];
+  __shared__ int last;
+  const int t = threadIdx.x, lane = t & 31, jg = t >> 5;
+  after_previous();
+  {
+    const int b = blockIdx.x * JG + jg;
+    bool act = false;
+    uint32_t kk = 0;
+    if (b < a.tiles - 1) {
+      const long long pe = ((long long)b + 1) * a.R, p0 = pe - a.R;   // the tile is [p0, pe)
+      kk = a.keys[pe - 1];
+      const uint32_t behind = a.keys[pe], before = p0 > 0 ? a.keys[p0 - 1] : 0xffffffffu;
+      act = behind == kk && before != kk && kk < (uint32_t)a.V;
+    }
+    bool lng = false;
+    if (act) {   // uniform in the warp
+      const int q = b + 1 + lane;
+      // the first tile behind that does not end with the id, and whether it starts with it
+      const bool ends = q >= a.tiles - 1 || a.keys[((long long)q + 1) * a.R - 1] != kk;
+      const bool starts = q < a.tiles && a.keys[(long long)q * a.R] == kk;
+      const uint32_t e = __ballot_sync(0xffffffffu, ends), f = __ballot_sync(0xffffffffu, starts);
+      lng = e == 0;
+      if (!lng) {
+        const int i = __ffs(e) - 1, n = (f >> i & 1) ? i + 1 : i;   // head rows
+        for (int col = blockIdx.y * 32 + lane; col < a.D; col += gridDim.y * 32) {
+          float s[1] = {a.tail[(size_t)b * a.D + col]};
+#pragma unroll 4
+          for (int k = 1; k <= n; ++k) s[0] += a.head[(size_t)(b + k) * a.D + col];
+          write_sum<1>(a, kk, col, s);
+        }
+      }
+    }
+    if (lane == 0) todo[jg] = lng;
   }
-  const int tl = (int)((lo - 1) / a.R);                     // the run's last tile
-  for (int c0 = blockIdx.y * 32; c0 < a.D; c0 += gridDim.y * 32) {
-    const int col = c0 + lane;
-    float s = 0.f;
-    if (col < a.D) {
-      if (jg == 0) s = a.tail[(size_t)blockIdx.x * a.D + col];
-#pragma unroll 8
-      for (int q = (int)blockIdx.x + 1 + jg; q <= tl; q += JG) s += a.head[(size_t)q * a.D + col];
+  __syncthreads();
+  for (int j = 0; j < JG; ++j) {
+    if (!todo[j]) continue;
+    const int b = blockIdx.x * JG + j;
+    const uint32_t kk = a.keys[((long long)b + 1) * a.R - 1];
+    for (int q0 = b + 1;; q0 += 32 * JG) {
+      const int q = q0 + t;
+      const bool ends = q >= a.tiles - 1 || a.keys[((long long)q + 1) * a.R - 1] != kk;
+      if (t == 0) last = INT32_MAX;
+      __syncthreads();
+      if (ends) atomicMin(&last, q);
+      __syncthreads();
+      if (last != INT32_MAX) break;
     }
-    part[jg][lane] = s;
-    __syncthreads();
-    if (jg == 0 && col < a.D) {
-      float acc = part[0][lane];
+    int tl = last;
+    if (a.keys[(long long)tl * a.R] != kk) --tl;   // it may not even start with the id
+    for (int c0 = blockIdx.y * 32; c0 < a.D; c0 += gridDim.y * 32) {
+      const int col = c0 + lane;
+      float s = 0.f;
+      if (col < a.D) {
+        if (jg == 0) s = a.tail[(size_t)b * a.D + col];
+#pragma unroll 16
+        for (int q = b + 1 + jg; q <= tl; q += JG) s += a.head[(size_t)q * a.D + col];
+      }
+      part[jg][lane] = s;
+      __syncthreads();
+      if (jg == 0 && col < a.D) {
+        float one[1] = {part[0][lane]};
 #pragma unroll
-      for (int j = 1; j < JG; ++j) acc += part[j][lane];
-      float one[1] = {acc};
-      write_sum<1>(a, kk, col, one);
+        for (int i = 1; i < JG; ++i) one[0] += part[i][lane];
+        write_sum<1>(a, kk, col, one);
+      }
+      __syncthreads();
     }
-    __syncthreads();
   }
 }
 
@@ -499,13 +564,172 @@ static e2f_status launch_reduce(RedArgs a, const T *g, cudaStream_t s) {
   const int dv = (a.D + VE - 1) / VE;
   const int RG = NT / a.CL;
   const size_t smem = sizeof(int) * (size_t)(2 * a.R + 2 + 2 * NT * VE + RG);
-  const int zero = a.accumulate ? 0 : (a.V + ZROWS - 1) / ZROWS;
-  dim3 grid((unsigned)(a.tiles + zero), (unsigned)((dv + a.CL - 1) / a.CL));
-  E2F_LAUNCH((reduce_kernel<T, VE>), grid, NT, smem, s, a, g);
+  dim3 grid((unsigned)a.tiles, (unsigned)((dv + a.CL - 1) / a.CL));
+  E2F_LAUNCH_AFTER((reduce_kernel<T, VE>), grid, NT, smem, s, a, g);
   if (a.tiles > 1) {
-    dim3 cg((unsigned)(a.tiles - 1), (unsigned)std::min(64, (a.D + 31) / 32));
-    E2F_LAUNCH(combine_kernel, cg, 32 * JG, 0, s, a);
+    dim3 cg((unsigned)((a.tiles - 1 + JG - 1) / JG), (unsigned)std::min(64, (a.D + 31) / 32));
+    E2F_LAUNCH_AFTER(combine_kernel, cg, 32 * JG, 0, s, a);
   }
+  return E2F_OK;
+}
+
+// ---------------------------------------------------------------------------
+// Few rows: one kernel.  A CTA has the ids [v0, v0 + W) and a block of columns:
+// it ranks the rows of its ids as a radix pass does (digit: id - v0), keeps them
+// sorted in shared memory and sums each id's rows, a warp to a short list, the
+// whole CTA to a long one.  No scratch, one launch: latency is what it costs.
+// ---------------------------------------------------------------------------
+constexpr int SMALL_N = 1024, SMALL_W = 256, LONG_LIST = 64;
+
+template <typename I, typename T, int VE>
+__global__ void __launch_bounds__(NT) small_kernel(RedArgs a, int W, const I *__restrict__ ids, const T *__restrict__ g,
+                                                   int *err) {
+  constexpr int NW = NT / 32;
+  __shared__ int cnt[NW][SMALL_W];
+  __shared__ int start[SMALL_W + 1];
+  __shared__ int srow[SMALL_N];
+  __shared__ float part[NW][32 * VE];
+  __shared__ int longs[SMALL_N / LONG_LIST], nlong;
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  const int v0 = blockIdx.x * W, nw = min(W, a.V - v0);
+  for (int i = t; i < NW * SMALL_W; i += NT) cnt[0][i] = 0;
+  __syncthreads();
+  // warp w ranks the rows [w per, (w + 1) per)
+  constexpr int PER = SMALL_N / NT;
+  const int per = (a.N + NW * 32 - 1) / (NW * 32) * 32;
+  int key[PER], rank[PER];
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    const int i = warp * per + j * 32 + lane;
+    key[j] = -1;
+    if (j * 32 < per && i < a.N) {
+      const long long id = (long long)ids[i];
+      if (id >= v0 && id < v0 + nw) key[j] = (int)(id - v0);
+      else if ((id < -1 || id >= a.V) && blockIdx.x == 0 && blockIdx.y == 0) atomicExch(err, E2F_ERR_DOMAIN);
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    rank[j] = 0;
+    if (j * 32 >= per || !__any_sync(0xffffffffu, key[j] >= 0)) continue;
+    const uint32_t same = __match_any_sync(0xffffffffu, key[j]);
+    int before = 0;
+    if (key[j] >= 0) before = cnt[warp][key[j]];
+    __syncwarp();
+    rank[j] = before + __popc(same & ((1u << lane) - 1u));
+    if (key[j] >= 0 && (same >> lane) == 1u) cnt[warp][key[j]] = before + __popc(same);
+    __syncwarp();
+  }
+  __syncthreads();
+  // start[d]: rows of smaller ids; cnt[w][d]: first place of warp w's rows of id d
+  {
+    int total = 0;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) total += cnt[w][t];
+    int incl = total;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int u = __shfl_up_sync(0xffffffffu, incl, o);
+      if (lane >= o) incl += u;
+    }
+    __shared__ int wsum[NW];
+    if (lane == 31) wsum[warp] = incl;
+    __syncthreads();
+    int off = 0;
+    for (int w = 0; w < warp; ++w) off += wsum[w];
+    int run = off + incl - total;
+    start[t] = run;
+    if (t == SMALL_W - 1) start[SMALL_W] = run + total;
+#pragma unroll
+    for (int w = 0; w < NW; ++w) {
+      const int c = cnt[w][t];
+      cnt[w][t] = run;
+      run += c;
+    }
+  }
+  __syncthreads();
+#pragma unroll
+  for (int j = 0; j < PER; ++j)
+    if (key[j] >= 0) srow[cnt[warp][key[j]] + rank[j]] = warp * per + j * 32 + lane;
+  __syncthreads();
+  // CL lanes over the columns, S = 32 / CL rows side by side
+  const int CL = a.CL, S = 32 / CL, cl = lane % CL, sub = lane / CL;
+  const int col = (blockIdx.y * CL + cl) * VE;
+  const bool in = col < a.D;
+  auto warp_rows = [&](int i0, int i1, float (&acc)[VE]) {
+#pragma unroll
+    for (int k = 0; k < VE; ++k) acc[k] = 0.f;
+    constexpr int U = VE == 8 ? 4 : 8;
+    for (int i = i0 + sub; i < i1; i += U * S) {
+      float v[U][VE];
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+#pragma unroll
+        for (int k = 0; k < VE; ++k) v[u][k] = 0.f;
+        if (i + u * S < i1 && in) Vec<T, VE>::load(g + (size_t)srow[i + u * S] * a.ld + col, v[u]);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int k = 0; k < VE; ++k) acc[k] += v[u][k];
+    }
+    for (int o = CL; o < 32; o <<= 1)
+#pragma unroll
+      for (int k = 0; k < VE; ++k) acc[k] += __shfl_xor_sync(0xffffffffu, acc[k], o);
+  };
+  // short lists, and zeros for the ids that do not occur
+  const int c0 = blockIdx.y * CL * VE, cw = min(CL * VE, a.D - c0);
+  if (t == 0) nlong = 0;
+  __syncthreads();
+  float acc[VE];
+  for (int d = warp; d < nw; d += NW) {
+    const int i0 = start[d], n = start[d + 1] - i0;
+    if (n == 0) {
+      if (a.accumulate) continue;
+      float *p = a.grad + (size_t)(v0 + d) * a.D + c0;
+      if (VE >= 4 && a.gvec)
+        for (int c = lane; c < cw / 4; c += 32) reinterpret_cast<float4 *>(p)[c] = make_float4(0.f, 0.f, 0.f, 0.f);
+      else
+        for (int c = lane; c < cw; c += 32) p[c] = 0.f;
+    } else if (n <= LONG_LIST) {
+      warp_rows(i0, i0 + n, acc);
+      if (sub == 0 && in) write_sum<VE>(a, (uint32_t)(v0 + d), col, acc);
+    } else if (lane == 0) {
+      longs[atomicAdd(&nlong, 1)] = d;
+    }
+  }
+  __syncthreads();
+  for (int l = 0; l < nlong; ++l) {   // (any order: each id's sum stands alone)
+    const int d = longs[l], n = start[d + 1] - start[d];
+    const int piece = (n + NW - 1) / NW, i0 = start[d] + min(n, warp * piece), i1 = start[d] + min(n, (warp + 1) * piece);
+    warp_rows(i0, i1, acc);
+    __syncthreads();
+    if (sub == 0)
+#pragma unroll
+      for (int k = 0; k < VE; ++k) part[warp][cl * VE + k] = acc[k];
+    __syncthreads();
+    if (warp == 0 && sub == 0 && in) {
+#pragma unroll
+      for (int w = 1; w < NW; ++w)
+#pragma unroll
+        for (int k = 0; k < VE; ++k) acc[k] += part[w][cl * VE + k];
+      write_sum<VE>(a, (uint32_t)(v0 + d), col, acc);
+    }
+  }
+}
+
+template <typename I, typename T, int VE>
+static e2f_status launch_small(RedArgs a, const I *ids, const T *g, int *err, cudaStream_t s) {
+  const int dv = (a.D + VE - 1) / VE;
+  // Enough CTAs for the device: ids first, then blocks of eight vectors of
+  // columns instead of 32 where there are few ids.
+  const int W = std::min(SMALL_W, std::max(1, (a.V + 591) / 592));
+  const int ctas = (a.V + W - 1) / W;
+  const int widest = ctas * ((dv + 31) / 32) < 296 ? 8 : 32;
+  a.CL = 1;
+  while (a.CL < widest && a.CL < dv) a.CL <<= 1;
+  dim3 grid((unsigned)ctas, (unsigned)((dv + a.CL - 1) / a.CL));
+  E2F_LAUNCH((small_kernel<I, T, VE>), grid, NT, 0, s, a, W, ids, g, err);
   return E2F_OK;
 }
 
@@ -524,10 +748,22 @@ static e2f_status backward(const I *ids, int64_t N64, const T *g, int64_t V, int
   const int VE = D % W == 0 && aligned_to(g, 16) ? W : (D % 2 == 0 && aligned_to(g, 2 * sizeof(T)) ? 2 : 1);
   RedArgs a{};
   a.N = N; a.V = (int)V; a.D = D; a.ld = ld; a.scale = scale; a.accumulate = accumulate; a.grad = grad;
+  a.gvec = D % 4 == 0 && aligned_to(grad, 16);
+  if (N <= SMALL_N) {
+    if (VE == W) return launch_small<I, T, W>(a, ids, g, err, s);
+    if (VE == 2) return launch_small<I, T, 2>(a, ids, g, err, s);
+    return launch_small<I, T, 1>(a, ids, g, err, s);
+  }
   const int dv = (D + VE - 1) / VE;
-  a.CL = 1;
+  a.CL = 8;   // eight lanes at least: the row groups are joined one after another
   while (a.CL < 32 && a.CL < dv) a.CL <<= 1;
-  a.R = std::min(1024, 32 * (NT / a.CL));
+  // rows of a group: a multiple of eight (batches of loads) that lets one wave
+  // of CTAs cover everything, 32 at most (100,002 rows, D = 128: 24 rows 12 us,
+  // 16 rows, a wave and a bit, 18 us)
+  const int RG = NT / a.CL;
+  const long long cols = (dv + a.CL - 1) / a.CL, slots = 148 * RED_CTAS;
+  const int G = (int)std::min<long long>(32, 8 * (((N + 8LL * RG - 1) / (8LL * RG) * cols + slots - 1) / slots));
+  a.R = std::min(1024, RG * G);
   a.tiles = (N + a.R - 1) / a.R;
   SortArgs sa{};
   sa.N = N; sa.V = (int)V;
@@ -545,11 +781,28 @@ static e2f_status backward(const I *ids, int64_t N64, const T *g, int64_t V, int
   a.tail = reinterpret_cast<float *>(w + 4 * kb + pb);
   int *hist = reinterpret_cast<int *>(w + 4 * kb + 2 * pb);
   // keys run over 0 .. V (V: rows that take no part)
-  E2F_LAUNCH((hist_kernel<I, true>), st, NT, 0, s, sa, ids, nullptr, hist, err);
-  E2F_LAUNCH((scatter_kernel<I, true>), st, NT, 0, s, sa, ids, nullptr, nullptr, hist, k0, q0);
-  for (sa.shift = 8; sa.shift < 32 && ((uint64_t)V >> sa.shift) != 0; sa.shift += 8) {
-    E2F_LAUNCH((hist_kernel<I, false>), st, NT, 0, s, sa, nullptr, k0, hist, err);
-    E2F_LAUNCH((scatter_kernel<I, false>), st, NT, 0, s, sa, nullptr, k0, q0, hist, k1, q1);
+  int passes = 1;
+  while (8 * passes < 32 && ((uint64_t)V >> (8 * passes)) != 0) ++passes;
+  sa.tiles = st;
+  // an equal part of the table is zeroed beside each of the sort's kernels
+  const size_t total = accumulate ? 0 : (size_t)V * D, part = ((total + 2 * passes - 1) / (2 * passes) + 3) & ~(size_t)3;
+  const unsigned zc = (unsigned)std::min<size_t>((part + 16383) / 16384, 592);
+  int k = 0;
+  auto next_zero = [&] {
+    sa.z0 = grad + std::min(total, k * part);
+    sa.z1 = grad + std::min(total, (k + 1) * part);
+    ++k;
+  };
+  next_zero();
+  E2F_LAUNCH((hist_kernel<I, true>), st + zc, NT, 0, s, sa, ids, nullptr, hist, err);
+  next_zero();
+  E2F_LAUNCH_AFTER((scatter_kernel<I, true>), st + zc, NT, 0, s, sa, ids, nullptr, nullptr, hist, k0, q0);
+  for (int pass = 1; pass < passes; ++pass) {
+    sa.shift = 8 * pass;
+    next_zero();
+    E2F_LAUNCH_AFTER((hist_kernel<I, false>), st + zc, NT, 0, s, sa, nullptr, k0, hist, err);
+    next_zero();
+    E2F_LAUNCH_AFTER((scatter_kernel<I, false>), st + zc, NT, 0, s, sa, nullptr, k0, q0, hist, k1, q1);
     std::swap(k0, k1);
     std::swap(q0, q1);
   }

@@ -357,17 +357,20 @@ __global__ void __launch_bounds__(256) colsum_kernel(const float *__restrict__ p
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
-static int sm_count() {
-  int dev = 0, n = 148;
-  if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev);
+static int sm_count() {   // one kind of device
+  static const int n = [] {
+    int dev = 0, v = 148;
+    if (cudaGetDevice(&dev) == cudaSuccess) cudaDeviceGetAttribute(&v, cudaDevAttrMultiProcessorCount, dev);
+    return v;
+  }();
   return n;
 }
 
 template <typename T, bool AMN, bool BMN> static e2f_status launch_staged(const Gemm &g, dim3 grid, cudaStream_t s) {
   int *err = device_error_flag();
   if (!err) return E2F_ERR_CUDA;
-  auto k = gemm_staged_kernel<T, AMN, BMN>;
-  E2F_CUDA_TRY(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)staged_smem<T>()));
+  constexpr auto k = gemm_staged_kernel<T, AMN, BMN>;
+  E2F_CUDA_TRY(allow_smem<k>(staged_smem<T>()));
   E2F_LAUNCH(k, grid, NT, staged_smem<T>(), s, g, err);
   return E2F_OK;
 }

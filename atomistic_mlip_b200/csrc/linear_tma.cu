@@ -486,8 +486,8 @@ static bool encode(CUtensorMap *m, const void *p, long long rows, long long cols
 
 template <bool AMN, bool BMN, int BN, bool LONGK, int EPI, int EW>
 static e2f_status launch_epi(const CUtensorMap &ta, const CUtensorMap &tb, const Args &a, int sms, cudaStream_t s) {
-  auto k = gemm_tma_kernel<AMN, BMN, BN, LONGK, EPI, EW>;
-  E2F_CUDA_TRY(cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem_bytes<EW>()));
+  constexpr auto k = gemm_tma_kernel<AMN, BMN, BN, LONGK, EPI, EW>;
+  E2F_CUDA_TRY(allow_smem<k>(smem_bytes<EW>()));
   E2F_LAUNCH(k, std::min(a.tiles, sms), threads<EW>(), smem_bytes<EW>(), s, ta, tb, a);
   return E2F_OK;
 }

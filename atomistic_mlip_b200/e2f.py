@@ -379,56 +379,55 @@ def attention_backward(x, pos, nl: NeighborList, w: DeviceWeights, grad_out, str
 # ----------------------------------------------------------------------------
 # the two ends of a model
 # ----------------------------------------------------------------------------
-_CODES = None
+_CODES = {}
 
 
 def _code(t, what: str, kinds: str) -> int:
     """Type code of a tensor for the C ABI; `kinds` 'f' (float32, bfloat16) or
     'i' (int32, int64)."""
-    global _CODES
-    if _CODES is None:
+    if not _CODES:
         torch = _torch()
-        _CODES = {"f": {torch.float32: F32, torch.bfloat16: BF16}, "i": {torch.int32: I32, torch.int64: I64}}
-    dt = t if not hasattr(t, "dtype") else t.dtype
-    code = _CODES[kinds].get(dt)
+        _CODES.update({("f", torch.float32): F32, ("f", torch.bfloat16): BF16, ("i", torch.int32): I32,
+                       ("i", torch.int64): I64})
+    code = _CODES.get((kinds, t.dtype))
     if code is None:
-        raise ValueError(f"{what} has type {dt}")
+        raise ValueError(f"{what} has type {t.dtype}")
     return code
 
 
-class _On:
-    """The device of a call's tensors and its stream: every tensor must be on
-    one CUDA device; the library works on the current one, so a call for
-    another device makes that the current one while it runs."""
-    __slots__ = ("stream", "_ctx")
+def _same_device(**tensors) -> int:
+    """Index of the one CUDA device that holds the tensors."""
+    first = dev = None
+    for name, t in tensors.items():
+        if t is None:
+            continue
+        d = t.get_device()
+        if d < 0:
+            raise ValueError(f"{name} is not on a CUDA device")
+        if dev is None:
+            first, dev = name, d
+        elif d != dev:
+            raise ValueError(f"{name} is on device {d}, {first} on device {dev}")
+    return dev
 
-    def __init__(self, stream, **tensors):
-        torch = _torch()
-        dev = None
-        for name, t in tensors.items():
-            if t is None:
-                continue
-            if not t.is_cuda:
-                raise ValueError(f"{name} is not on a CUDA device")
-            if dev is None:
-                dev, first = t.device, name
-            elif t.device != dev:
-                raise ValueError(f"{name} is on {t.device}, {first} on {dev}")
-        self._ctx = None if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
-        if stream is None:
-            stream = torch.cuda.current_stream(dev)
-        elif stream.device != dev:
-            raise ValueError(f"the stream is on {stream.device}, {first} on {dev}")
-        self.stream = stream.cuda_stream
 
-    def __enter__(self):
-        if self._ctx is not None:
-            self._ctx.__enter__()
-        return self.stream
-
-    def __exit__(self, *exc):
-        if self._ctx is not None:
-            self._ctx.__exit__(*exc)
+def _call(dev: int, stream, fn: str, *args):
+    """A library call on device `dev` (made the current one while it runs) and
+    on `stream`, or that device's current stream."""
+    torch = _torch()
+    if stream is None:
+        s = torch._C._cuda_getCurrentRawStream(dev)
+    elif stream.device_index != dev:
+        raise ValueError(f"the stream is on device {stream.device_index}, the tensors on device {dev}")
+    else:
+        s = stream.cuda_stream
+    if torch.cuda.current_device() == dev:
+        code = getattr(lib(), fn)(*args, s)
+    else:
+        with torch.cuda.device(dev):
+            code = getattr(lib(), fn)(*args, s)
+    if code:
+        _check(code, fn)
 
 
 def _need(cond, msg: str):
@@ -452,10 +451,8 @@ def embed_forward(ids, table, scale: float = 1.0, Q: int = 1, out_dtype=None, ou
     else:
         _need(out.shape == (N, Q, D) and out.is_contiguous(), f"out must be contiguous {(N, Q, D)}")
         _need(out_dtype is None or out.dtype == out_dtype, "out has another type than out_dtype")
-    with _On(stream, ids=ids, table=table, out=out) as s:
-        code = lib().e2f_embed_forward(_ptr(ids), it, N, _ptr(table), tt, V, D, scale, Q, _ptr(out),
-                                       _code(out, "out", "f"), s)
-    _check(code, "e2f_embed_forward")
+    _call(_same_device(ids=ids, table=table, out=out), stream, "e2f_embed_forward", ids.data_ptr(), it, N,
+          table.data_ptr(), tt, V, D, scale, Q, out.data_ptr(), _code(out, "out", "f"))
     return out
 
 
@@ -477,10 +474,8 @@ def embed_backward(ids, grad_out, V: int, scale: float = 1.0, grad_table=None, a
     else:
         _need(grad_table.shape == (V, D) and grad_table.is_contiguous() and grad_table.dtype == torch.float32,
               f"grad_table must be contiguous float32 {(V, D)}")
-    with _On(stream, ids=ids, grad_out=grad_out, grad_table=grad_table) as s:
-        code = lib().e2f_embed_backward(_ptr(ids), it, N, _ptr(grad_out), gt, V, D, scale, Q, _ptr(grad_table),
-                                        1 if accumulate else 0, s)
-    _check(code, "e2f_embed_backward")
+    _call(_same_device(ids=ids, grad_out=grad_out, grad_table=grad_table), stream, "e2f_embed_backward",
+          ids.data_ptr(), it, N, grad_out.data_ptr(), gt, V, D, scale, Q, grad_table.data_ptr(), int(bool(accumulate)))
     return grad_table
 
 
@@ -529,9 +524,8 @@ def linear_forward(x, W, bias=None, residual=None, act: str = "none", out=None, 
     if residual is not None:
         ldr = _ld(residual, M, N, "residual")
         _need(residual.dtype == out.dtype, f"residual has type {residual.dtype}, the output {out.dtype}")
-    with _On(stream, x=x, W=W, bias=bias, residual=residual, out=out) as s:
-        code = lib().e2f_linear_forward(ctypes.byref(p), _ptr(residual), ldr, _ptr(out), ldo, _code(out, "out", "f"), s)
-    _check(code, "e2f_linear_forward")
+    _call(_same_device(x=x, W=W, bias=bias, residual=residual, out=out), stream, "e2f_linear_forward",
+          ctypes.byref(p), _ptr(residual), ldr, out.data_ptr(), ldo, _code(out, "out", "f"))
     return out
 
 
@@ -559,10 +553,9 @@ def linear_backward(x, W, grad_out, bias=None, act: str = "none", need_x: bool =
     if grad_W is not None:
         ldgw = _ld(grad_W, N, K, "grad_W")
         _need(grad_W.dtype == x.dtype, f"grad_W has type {grad_W.dtype}, x {x.dtype}")
-    with _On(stream, x=x, W=W, bias=bias, grad_out=grad_out, grad_x=grad_x, grad_W=grad_W) as s:
-        code = lib().e2f_linear_backward(ctypes.byref(p), _ptr(grad_out), ldg, _code(grad_out, "grad_out", "f"),
-                                         _ptr(grad_x), ldgx, _ptr(grad_W), ldgw, _ptr(gb), s)
-    _check(code, "e2f_linear_backward")
+    _call(_same_device(x=x, W=W, bias=bias, grad_out=grad_out, grad_x=grad_x, grad_W=grad_W), stream,
+          "e2f_linear_backward", ctypes.byref(p), grad_out.data_ptr(), ldg, _code(grad_out, "grad_out", "f"),
+          _ptr(grad_x), ldgx, _ptr(grad_W), ldgw, _ptr(gb))
     return grad_x, grad_W, gb
 
 

@@ -64,6 +64,8 @@ BWD = [  # N, V, D, Q, kind
     (4097, 70001, 257, 1, "uniform"), (20001, 7, 1, 1, "sorted"), (20001, 1, 1, 1, "one"), (20001, 2, 16, 1, "species"),
     (9000, 40, 768, 1, "species"), (300, 119, 128, 9, "all_padded"), (60000, 119, 128, 1, "one"),
     (30011, 1000, 24, 1, "padded"), (12000, 3, 1000, 1, "uniform"),
+    (4096, 3, 130, 1, "species"), (3000, 119, 128, 25, "species"), (4096, 60000, 40, 1, "uniform"),
+    (4097, 5, 12, 1, "padded"), (1024, 119, 128, 25, "species"), (1023, 3, 770, 1, "padded"), (1000, 60000, 12, 1, "uniform"), (200000, 2, 8, 1, "species"), (70000, 66000, 16, 1, "one"),
 ]
 
 
