@@ -68,13 +68,21 @@ inline cudaError_t launch_after(void (*k)(P...), dim3 grid, dim3 block, size_t s
 
 // Dynamic shared memory of kernel K (always the same size), allowed once per
 // device: the attribute call costs as much host time as a quarter of a launch.
-template <auto K> cudaError_t allow_smem(size_t bytes) {
+// regs: registers a thread that K must have been compiled to (a kernel that
+// redistributes them with setmaxnreg would wait for ever with fewer).
+template <auto K> cudaError_t allow_smem(size_t bytes, int regs = 0) {
   static std::atomic<uint64_t> done{0};
   int dev = 0;
   cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
   const uint64_t bit = 1ull << (dev & 63);
   if (done.load(std::memory_order_relaxed) & bit) return cudaSuccess;
+  if (regs) {
+    cudaFuncAttributes at;
+    e = cudaFuncGetAttributes(&at, K);
+    if (e != cudaSuccess) return e;
+    if (at.numRegs != regs) return cudaErrorInvalidDeviceFunction;
+  }
   e = cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
   if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
   return e;

@@ -24,255 +24,10 @@ namespace lin {
 bool tma_operand(const void *p, long long ld);
 template <bool AMN, bool BMN> e2f_status gemm_tma(const Gemm &g, int splits, int bn, int sms, cudaStream_t s);
 
+// linear_reg.cu
+template <typename T, bool AMN, bool BMN> e2f_status gemm_reg(const Gemm &g, int splits, int bn, int sms, cudaStream_t s);
+
 constexpr int BM = 128, BN = 128, BK = 64, NT = 256;
-constexpr int TILE_BYTES = 128 * BK * 2;     // one 128 x 64 bf16 operand tile
-constexpr int EPITCH = BN + 1;               // accumulator tile in shared memory, floats per row
-
-// ---------------------------------------------------------------------------
-// operand tiles: 128 x 64 bf16 in 128-byte swizzled rows.  K-major: a row
-// holds 64 k.  MN-major: two blocks of 64 m, a row holds the 64 m of one k.
-// ---------------------------------------------------------------------------
-template <bool MN> __device__ __forceinline__ uint32_t chunk_off(int q) {
-  if (!MN) {   // chunk of 8 k
-    const int r = q >> 3, c = q & 7;
-    return (uint32_t)(r * 128 + ((c ^ (r & 7)) << 4));
-  }
-  const int k = q >> 4, c = q & 15;   // chunk of 8 m
-  return (uint32_t)((c >> 3) * 8192 + k * 128 + (((c & 7) ^ (k & 7)) << 4));
-}
-
-// Descriptor of such a tile from the k-th (multiple of 16) column on: 128-byte
-// swizzle, 1024 bytes from eight rows to the next; MN-major: 8192 bytes from
-// one block of 64 m to the next.
-template <bool MN> __device__ __forceinline__ uint64_t tile_desc(uint32_t saddr, int k) {
-  const uint32_t a = saddr + (MN ? k * 128 : k * 2);
-  return tc::smem_desc(a, MN ? 8192 : 16, 1024) | (uint64_t)2 << 61;
-}
-
-// Eight consecutive elements of an operand; nv of them are inside.
-template <typename T> struct Raw;
-template <> struct Raw<__nv_bfloat16> { uint4 a; };
-template <> struct Raw<float> { float4 a, b; };
-
-__device__ __forceinline__ void load8(Raw<__nv_bfloat16> &r, const __nv_bfloat16 *p, int nv, bool vec) {
-  if (vec && nv >= 8) {
-    r.a = __ldg(reinterpret_cast<const uint4 *>(p));
-    return;
-  }
-  const unsigned short *u = reinterpret_cast<const unsigned short *>(p);
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const uint32_t lo = 2 * i < nv ? __ldg(u + 2 * i) : 0u, hi = 2 * i + 1 < nv ? __ldg(u + 2 * i + 1) : 0u;
-    w[i] = lo | hi << 16;
-  }
-  r.a = make_uint4(w[0], w[1], w[2], w[3]);
-}
-__device__ __forceinline__ void load8(Raw<float> &r, const float *p, int nv, bool vec) {
-  if (vec && nv >= 8) {
-    r.a = __ldg(reinterpret_cast<const float4 *>(p));
-    r.b = __ldg(reinterpret_cast<const float4 *>(p) + 1);
-    return;
-  }
-  float v[8];
-#pragma unroll
-  for (int i = 0; i < 8; ++i) v[i] = i < nv ? __ldg(p + i) : 0.f;
-  r.a = make_float4(v[0], v[1], v[2], v[3]);
-  r.b = make_float4(v[4], v[5], v[6], v[7]);
-}
-
-// Terms of a chunk to shared memory, TILE_BYTES apart.
-__device__ __forceinline__ void put8(const Raw<__nv_bfloat16> &r, uint8_t *p) { *reinterpret_cast<uint4 *>(p) = r.a; }
-__device__ __forceinline__ void split2(float x, float y, uint32_t &h, uint32_t &m, uint32_t &l) {
-  h = pack_bf16x2(x, y);
-  x -= __uint_as_float(h << 16);
-  y -= __uint_as_float(h & 0xffff0000u);
-  m = pack_bf16x2(x, y);
-  x -= __uint_as_float(m << 16);
-  y -= __uint_as_float(m & 0xffff0000u);
-  l = pack_bf16x2(x, y);
-}
-__device__ __forceinline__ void put8(const Raw<float> &r, uint8_t *p) {
-  uint4 h, m, l;
-  split2(r.a.x, r.a.y, h.x, m.x, l.x);
-  split2(r.a.z, r.a.w, h.y, m.y, l.y);
-  split2(r.b.x, r.b.y, h.z, m.z, l.z);
-  split2(r.b.z, r.b.w, h.w, m.w, l.w);
-  *reinterpret_cast<uint4 *>(p) = h;
-  *reinterpret_cast<uint4 *>(p + TILE_BYTES) = m;
-  *reinterpret_cast<uint4 *>(p + 2 * TILE_BYTES) = l;
-}
-
-// The chunks of one operand tile this thread carries: rows r0.. (m or n),
-// contraction k0..; RN rows and KN columns exist.
-template <typename T, bool MN>
-__device__ __forceinline__ void fetch_tile(Raw<T> (&r)[4], const T *P, long long ld, int r0, int RN, int k0, int KN,
-                                           bool vec) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const int q = threadIdx.x + NT * j;
-    const int row = MN ? k0 + (q >> 4) : r0 + (q >> 3);          // strided index
-    const int col = MN ? r0 + 8 * (q & 15) : k0 + 8 * (q & 7);   // contiguous index
-    const int nrow = MN ? KN : RN, ncol = MN ? RN : KN;
-    const int nv = row < nrow ? ncol - col : 0;
-    load8(r[j], P + (nv > 0 ? (size_t)((long long)row * ld) + col : 0), nv, vec);
-  }
-}
-template <typename T, bool MN> __device__ __forceinline__ void put_tile(const Raw<T> (&r)[4], uint8_t *s) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) put8(r[j], s + chunk_off<MN>(threadIdx.x + NT * j));
-}
-
-// An element of the product from the fp32 operands themselves.
-template <bool AMN, bool BMN>
-__device__ __noinline__ float dot_again(const Gemm &g, int m, int n, int k0, int k1) {
-  const float *A = static_cast<const float *>(g.A), *B = static_cast<const float *>(g.B);
-  float s = 0.f;
-  for (int k = k0; k < k1; ++k)
-    s = fmaf(AMN ? A[(size_t)(k * g.lda) + m] : A[(size_t)(m * g.lda) + k],
-             BMN ? B[(size_t)(k * g.ldb) + n] : B[(size_t)(n * g.ldb) + k], s);
-  return s;
-}
-
-// ---------------------------------------------------------------------------
-// One 128 x 128 output tile per CTA (blockIdx: row tile, column tile, split of
-// the contraction).  All threads carry the operands global -> registers ->
-// shared memory (any stride and alignment; the fp32 form splits on the way),
-// two stages; the next block's loads are in flight while the tensor core works.
-// ---------------------------------------------------------------------------
-template <typename T> constexpr int terms() { return sizeof(T) == 4 ? 3 : 1; }
-template <typename T> constexpr size_t staged_smem() {
-  const size_t ops = 2 * (size_t)terms<T>() * 2 * TILE_BYTES, acc = sizeof(float) * BM * EPITCH;
-  return (ops > acc ? ops : acc) + 1024;
-}
-
-template <typename T, bool AMN, bool BMN>
-__global__ void __launch_bounds__(NT, 1) gemm_staged_kernel(const __grid_constant__ Gemm g, int *err) {
-  using namespace tc;
-  constexpr int NS = terms<T>();
-  constexpr int OP = NS * TILE_BYTES;          // one operand of a stage
-  constexpr uint32_t TCOLS = NS == 3 ? 256 : 128;
-  extern __shared__ uint8_t smem_raw[];
-  uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
-  __shared__ uint64_t bar[2];
-  __shared__ uint32_t tslot;
-  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
-  if (t == 0) { mbar_init(&bar[0], 1); mbar_init(&bar[1], 1); mbar_fence_init(); }
-  __syncthreads();
-  if (warp == 0) { tmem_alloc(&tslot, TCOLS); tmem_relinquish(); }
-  tc_fence_before();
-  __syncthreads();
-  tc_fence_after();
-  const uint32_t tb = tslot;
-  const int m0 = blockIdx.x * BM, n0 = blockIdx.y * BN;
-  const int nkb = (g.K + BK - 1) / BK;
-  const int kb0 = blockIdx.z * g.kper, kb1 = kb0 + g.kper < nkb ? kb0 + g.kper : nkb;
-  const T *A = static_cast<const T *>(g.A), *B = static_cast<const T *>(g.B);
-  const bool va = ((reinterpret_cast<uintptr_t>(A) | (uintptr_t)(g.lda * sizeof(T))) & 15) == 0;
-  const bool vb = ((reinterpret_cast<uintptr_t>(B) | (uintptr_t)(g.ldb * sizeof(T))) & 15) == 0;
-  const int nb = g.N - n0 < BN ? (g.N - n0 + 15) & ~15 : BN;   // columns the tensor core works on
-  const uint32_t id = idesc_bf16(128, nb, AMN, BMN);
-  Raw<T> ra[4], rb[4];
-  bool dead = false;
-  fetch_tile<T, AMN>(ra, A, g.lda, m0, g.M, kb0 * BK, g.K, va);
-  fetch_tile<T, BMN>(rb, B, g.ldb, n0, g.N, kb0 * BK, g.K, vb);
-  for (int kb = kb0; kb < kb1; ++kb) {
-    const int i = kb - kb0, st = i & 1;
-    uint8_t *sA = smem + st * 2 * OP, *sB = sA + OP;
-    if (i >= 2) {   // the products that read this stage two blocks ago are done
-      const bool ok = mbar_wait(&bar[st], ((i >> 1) - 1) & 1, 1u << 26);
-      dead = __syncthreads_or(!ok) != 0;
-      if (dead) break;
-    }
-    put_tile<T, AMN>(ra, sA);
-    put_tile<T, BMN>(rb, sB);
-    fence_async_smem();
-    __syncthreads();
-    if (t == 0) {
-      tc_fence_after();
-      const uint32_t a0 = smem_addr(sA), b0 = smem_addr(sB);
-#pragma unroll
-      for (int k = 0; k < BK; k += 16) {
-        const uint32_t first = i > 0 || k > 0 ? 1u : 0u;
-        mma_bf16_ss(tb, tile_desc<AMN>(a0, k), tile_desc<BMN>(b0, k), id, first);
-        if (NS == 3) {
-          const uint32_t am = a0 + TILE_BYTES, al = am + TILE_BYTES, bm = b0 + TILE_BYTES, bl = bm + TILE_BYTES;
-          mma_bf16_ss(tb + 128, tile_desc<AMN>(a0, k), tile_desc<BMN>(bl, k), id, first);
-          mma_bf16_ss(tb + 128, tile_desc<AMN>(al, k), tile_desc<BMN>(b0, k), id, 1u);
-          mma_bf16_ss(tb + 128, tile_desc<AMN>(am, k), tile_desc<BMN>(bm, k), id, 1u);
-          mma_bf16_ss(tb + 128, tile_desc<AMN>(a0, k), tile_desc<BMN>(bm, k), id, 1u);
-          mma_bf16_ss(tb + 128, tile_desc<AMN>(am, k), tile_desc<BMN>(b0, k), id, 1u);
-        }
-      }
-      mma_commit(&bar[st]);
-    }
-    if (kb + 1 < kb1) {
-      fetch_tile<T, AMN>(ra, A, g.lda, m0, g.M, (kb + 1) * BK, g.K, va);
-      fetch_tile<T, BMN>(rb, B, g.ldb, n0, g.N, (kb + 1) * BK, g.K, vb);
-    }
-  }
-  const int nblk = kb1 - kb0;
-  if (!dead) {   // a commit covers every product issued before it
-    const bool ok = mbar_wait(&bar[(nblk - 1) & 1], ((nblk - 1) >> 1) & 1, 1u << 26);
-    dead = __syncthreads_or(!ok) != 0;
-  }
-  if (dead) {
-    if (t == 0) atomicExch(err, E2F_ERR_TIMEOUT);
-  } else {
-    // accumulators -> shared memory (the operand stages are done with) -> rows
-    tc_fence_after();
-    float *acc = reinterpret_cast<float *>(smem);
-    {
-      const int row = 32 * (warp & 3) + lane, c0 = 64 * (warp >> 2);
-      const uint32_t ta = tb + ((uint32_t)(32 * (warp & 3)) << 16);
-#pragma unroll
-      for (int c = 0; c < 64; c += 16) {
-        if (c0 + c < nb) {
-          float v[16], w[16];
-          if (NS == 3) tmem_ld_32x32b_x16x2(ta + c0 + c, ta + 128 + c0 + c, v, w);
-          else tmem_ld_32x32b_x16(ta + c0 + c, v);
-#pragma unroll
-          for (int j = 0; j < 16; ++j) acc[row * EPITCH + c0 + c + j] = NS == 3 ? v[j] + w[j] : v[j];
-        }
-      }
-    }
-    __syncthreads();
-    float bias[4], csum[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int n = n0 + lane + 32 * j;
-      bias[j] = g.e.mode != MODE_PART && g.e.bias && n < g.N ? g.e.bias[n] : 0.f;
-      csum[j] = 0.f;
-    }
-    for (int r = warp; r < BM && m0 + r < g.M; r += NT / 32) {
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int n = n0 + lane + 32 * j;
-        if (n < g.N) {
-          float v = acc[r * EPITCH + lane + 32 * j];
-          if (NS == 3 && v != v) v = dot_again<AMN, BMN>(g, m0 + r, n, kb0 * BK, min(kb1 * BK, g.K));
-          if (g.e.mode == MODE_PART) g.part[((size_t)blockIdx.z * g.M + m0 + r) * g.N + n] = v;
-          else csum[j] += epi_elem(g.e, m0 + r, n, v, bias[j]);
-        }
-      }
-    }
-    if (g.e.mode == MODE_DZ && g.e.colpart) {
-      __syncthreads();
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[warp * BN + lane + 32 * j] = csum[j];
-      __syncthreads();
-      if (t < BN && n0 + t < g.N) {
-        float s = 0.f;
-#pragma unroll
-        for (int w = 0; w < NT / 32; ++w) s += acc[w * BN + t];
-        g.e.colpart[(size_t)blockIdx.x * g.N + n0 + t] = s;
-      }
-    }
-  }
-  tc_fence_before();
-  __syncthreads();
-  if (warp == 0) tmem_dealloc(tb, TCOLS);
-}
 
 // ---------------------------------------------------------------------------
 // Partial sums of a split contraction added in a fixed order, then the
@@ -366,16 +121,7 @@ static int sm_count() {   // one kind of device
   return n;
 }
 
-template <typename T, bool AMN, bool BMN> static e2f_status launch_staged(const Gemm &g, dim3 grid, cudaStream_t s) {
-  int *err = device_error_flag();
-  if (!err) return E2F_ERR_CUDA;
-  constexpr auto k = gemm_staged_kernel<T, AMN, BMN>;
-  E2F_CUDA_TRY(allow_smem<k>(staged_smem<T>()));
-  E2F_LAUNCH(k, grid, NT, staged_smem<T>(), s, g, err);
-  return E2F_OK;
-}
-
-// Row blocks whose column sums a MODE_DZ product leaves (upper bound).
+// Row blocks of 32 whose column sums a MODE_DZ product leaves.
 static int64_t colpart_rows(int64_t M) { return (M + FROWS - 1) / FROWS; }
 
 template <typename T, bool AMN, bool BMN> struct Path {
@@ -404,13 +150,15 @@ static e2f_status run_gemm(Gemm g, cudaStream_t s, int *rows_out = nullptr) {
   g.kper = (nkb + splits - 1) / splits;
   splits = (nkb + g.kper - 1) / g.kper;
   const bool tma = Path<T, AMN, BMN>::tma(g);
-  // TMA path: 128 x 256 tiles feed the tensor core at its full rate; 128 x 128
-  // where the wider ones would leave more of the last wave idle.
   int bn = BN;
   if (tma && g.N > BN && splits == 1) {
+    // TMA path: 128 x 256 tiles feed the tensor core at its full rate; 128 x
+    // 128 where the wider ones would leave more of the last wave idle.
     const long long nt2 = (g.N + 2 * BN - 1) / (2 * BN);
     const long long w1 = (tiles + sms - 1) / sms, w2 = (mt * nt2 + sms - 1) / sms;
     if (9 * w2 <= 5 * w1) bn = 2 * BN;
+  } else if (!tma && g.N > BN / 2 && tiles * splits * 2 <= sms) {
+    bn = BN / 2;   // half the tile's latency where SMs are idle anyway
   }
   const Epi e = g.e;
   Scratch ws;
@@ -420,8 +168,8 @@ static e2f_status run_gemm(Gemm g, cudaStream_t s, int *rows_out = nullptr) {
     g.e.mode = MODE_PART;
   }
   e2f_status st = tma ? Path<T, AMN, BMN>::run_tma(g, splits, bn, sms, s)
-                      : launch_staged<T, AMN, BMN>(g, dim3(mt, nt, splits), s);
-  if (rows_out) *rows_out = tma || splits > 1 ? (int)colpart_rows(g.M) : mt;
+                      : gemm_reg<T, AMN, BMN>(g, splits, bn, sms, s);
+  if (rows_out) *rows_out = (int)colpart_rows(g.M);
   if (st != E2F_OK || splits == 1) return st;
   const unsigned fy = (unsigned)((g.N + 31) / 32);
   if (e.mode == MODE_OUT && splits > 8) {
