@@ -66,6 +66,10 @@ inline cudaError_t launch_after(void (*k)(P...), dim3 grid, dim3 block, size_t s
     }                                                                                     \
   } while (0)
 
+// In a kernel launched behind another one of the same call: waits until what
+// that one wrote can be read.
+__device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+
 // Dynamic shared memory of kernel K (always the same size), allowed once per
 // device: the attribute call costs as much host time as a quarter of a launch.
 // regs: registers a thread that K must have been compiled to (a kernel that

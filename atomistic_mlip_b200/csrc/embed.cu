@@ -33,12 +33,6 @@ namespace emb {
 
 constexpr int NT = 256;
 
-// The kernels of one call start while the one before drains (programmatic
-// dependent launch) and wait here before they read what it wrote.
-__device__ __forceinline__ void after_previous() {
-  asm volatile("griddepcontrol.wait;" ::: "memory");
-}
-
 // VE consecutive elements of a row as floats (VE * sizeof(T) is 16, 4 or the
 // element's size; the caller guarantees that alignment).
 template <typename T, int VE> struct Vec;

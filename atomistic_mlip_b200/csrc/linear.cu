@@ -27,6 +27,9 @@ template <bool AMN, bool BMN> e2f_status gemm_tma(const Gemm &g, int splits, int
 // linear_reg.cu
 template <typename T, bool AMN, bool BMN> e2f_status gemm_reg(const Gemm &g, int splits, int bn, int sms, cudaStream_t s);
 
+// linear_skinny.cu
+template <typename T> e2f_status gemm_skinny(const Gemm &g, cudaStream_t s, int *rows_out);
+
 constexpr int BM = 128, BN = 128, BK = 64, NT = 256;
 
 // ---------------------------------------------------------------------------
@@ -40,6 +43,7 @@ constexpr int FROWS = 32;
 __global__ void __launch_bounds__(NT) finish_kernel(const float *__restrict__ part, int splits, int M, int N,
                                                     const __grid_constant__ Epi e) {
   __shared__ float red[NT / 32][33];
+  after_previous();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n = blockIdx.y * 32 + lane;
   const long long m0 = (long long)blockIdx.x * FROWS;
@@ -73,6 +77,7 @@ __global__ void __launch_bounds__(NT) finish_kernel(const float *__restrict__ pa
 __global__ void __launch_bounds__(NT) finish_row_kernel(const float *__restrict__ part, int splits, int M, int N,
                                                         const __grid_constant__ Epi e) {
   __shared__ float red[NT / 32][33];
+  after_previous();
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int n = blockIdx.y * 32 + lane, m = blockIdx.x;
   float v = 0.f;
@@ -88,23 +93,25 @@ __global__ void __launch_bounds__(NT) finish_row_kernel(const float *__restrict_
   }
 }
 
-// Column sums of P partial rows: a CTA takes 32 columns and CROWS rows, eight
-// interleaved sums joined in order; called again on its own partial rows until
-// one is left.
-constexpr int CROWS = 128;
-__global__ void __launch_bounds__(256) colsum_kernel(const float *__restrict__ part, int P, int N, float *__restrict__ out) {
-  __shared__ float red[8][32];
+// Column sums of P rows (of dz itself, or partial ones): a CTA takes 32 columns
+// and CROWS rows, 32 interleaved sums joined in order; called again on its own
+// partial rows until one is left.
+constexpr int CROWS = 1024;
+__global__ void __launch_bounds__(1024) colsum_kernel(const void *__restrict__ p, int type, long long ld, int P, int N,
+                                                      float *__restrict__ out) {
+  __shared__ float red[32][33];
+  after_previous();
   const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, n = blockIdx.x * 32 + lane;
   const int p0 = blockIdx.y * CROWS, p1 = min(p0 + CROWS, P);
   float s = 0.f;
   if (n < N)
 #pragma unroll 8
-    for (int p = p0 + w; p < p1; p += 8) s += part[(size_t)p * N + n];
+    for (int i = p0 + w; i < p1; i += 32) s += load_as(p, type, (size_t)(i * ld) + n);
   red[w][lane] = s;
   __syncthreads();
   if (w == 0 && n < N) {
 #pragma unroll
-    for (int j = 1; j < 8; ++j) s += red[j][lane];
+    for (int j = 1; j < 32; ++j) s += red[j][lane];
     out[(size_t)blockIdx.y * N + n] = s;
   }
 }
@@ -138,15 +145,18 @@ template <bool AMN, bool BMN> struct Path<__nv_bfloat16, AMN, BMN> {
 // A product with its epilogue.  rows_out: row blocks written to e.colpart.
 template <typename T, bool AMN, bool BMN>
 static e2f_status run_gemm(Gemm g, cudaStream_t s, int *rows_out = nullptr) {
+  if constexpr (!AMN && !BMN) {
+    if (g.M <= 8 || g.N <= 8) return gemm_skinny<T>(g, s, rows_out);
+  }
   const int mt = (g.M + BM - 1) / BM, nt = (g.N + BN - 1) / BN, nkb = (g.K + BK - 1) / BK;
-  if (nt > 65535) return E2F_ERR_UNSUPPORTED;
   // Fewer tiles than SMs: the contraction is split so that every SM has a
-  // tile, while each split keeps four blocks (below that the partial sums cost
-  // more than the shorter loop saves).
+  // tile, while each split keeps four blocks; contractions of up to 15 blocks
+  // stay whole (the partial sums' kernel costs more than the shorter loop
+  // saves).
   const long long tiles = (long long)mt * nt;
   const int sms = sm_count();
   int splits = 1;
-  if (tiles < sms && nkb >= 8) splits = (int)std::min<long long>(sms / tiles, nkb / 4);
+  if (tiles < sms && nkb >= 16) splits = (int)std::min<long long>(sms / tiles, nkb / 4);
   g.kper = (nkb + splits - 1) / splits;
   splits = (nkb + g.kper - 1) / g.kper;
   const bool tma = Path<T, AMN, BMN>::tma(g);
@@ -173,10 +183,10 @@ static e2f_status run_gemm(Gemm g, cudaStream_t s, int *rows_out = nullptr) {
   if (st != E2F_OK || splits == 1) return st;
   const unsigned fy = (unsigned)((g.N + 31) / 32);
   if (e.mode == MODE_OUT && splits > 8) {
-    E2F_LAUNCH(finish_row_kernel, dim3((unsigned)g.M, fy), NT, 0, s, g.part, splits, g.M, g.N, e);
+    E2F_LAUNCH_AFTER(finish_row_kernel, dim3((unsigned)g.M, fy), NT, 0, s, g.part, splits, g.M, g.N, e);
   } else {
     dim3 fg((unsigned)((g.M + FROWS - 1) / FROWS), fy);
-    E2F_LAUNCH(finish_kernel, fg, NT, 0, s, g.part, splits, g.M, g.N, e);
+    E2F_LAUNCH_AFTER(finish_kernel, fg, NT, 0, s, g.part, splits, g.M, g.N, e);
   }
   return E2F_OK;
 }
@@ -210,45 +220,58 @@ static e2f_status backward(const e2f_linear &p, const void *dy, int64_t ldg, int
   const long long lddz = (N + 7) & ~7;
   auto up = [](size_t b) { return (b + 255) & ~(size_t)255; };
   const size_t zb = own && prod ? up(sizeof(T) * (size_t)M * lddz) : 0;
-  // partial rows of the column sums, and one level of their sums
-  const int64_t cr = colpart_rows(M);
-  const size_t cb = gb ? sizeof(float) * (size_t)(cr + (cr + CROWS - 1) / CROWS) * N : 0;
+  // partial rows of the column sums, and two buffers for the sums of 1,024 rows each
+  const int64_t cr = own ? colpart_rows(M) : 0, cr2 = (std::max<int64_t>(cr, M) + CROWS - 1) / CROWS;
+  const size_t cb = gb ? sizeof(float) * (size_t)(cr + 2 * cr2) * N : 0;
   Scratch ws;
   if (zb + cb) E2F_CUDA_TRY(ws.alloc(zb + cb, s));
   const void *dz = dy;
   long long ldz = ldg;
-  int crows = 0;
-  if (own || gb) {
+  bool after = false;
+  // what the column sums are taken of
+  const void *cp = dy;
+  int ctype = out_dtype, crows = M;
+  long long cld = ldg;
+  if (own) {
     Gemm g{};
     g.A = p.x; g.lda = p.ldx; g.B = p.W; g.ldb = p.ldw;
     g.M = M; g.N = N; g.K = K;
     g.e.mode = MODE_DZ; g.e.act = p.act; g.e.bias = p.bias;
     g.e.extra = dy; g.e.lde = ldg; g.e.etype = out_dtype;
-    g.e.out = own && prod ? ws.p : nullptr; g.e.ldo = lddz; g.e.otype = TT;
+    g.e.out = prod ? ws.p : nullptr; g.e.ldo = lddz; g.e.otype = TT;
     g.e.colpart = gb ? reinterpret_cast<float *>(ws.as<char>() + zb) : nullptr;
+    crows = (int)cr;
     if (p.act != E2F_ACT_NONE) {
       e2f_status st = run_gemm<T, false, false>(g, s, &crows);
       if (st != E2F_OK) return st;
     } else {
-      dim3 fg((unsigned)((M + FROWS - 1) / FROWS), (unsigned)((N + 31) / 32));
       g.e.bias = nullptr;
-      E2F_LAUNCH(finish_kernel, fg, NT, 0, s, nullptr, 0, M, N, g.e);
-      crows = (int)fg.x;
+      E2F_LAUNCH(finish_kernel, dim3((unsigned)((M + FROWS - 1) / FROWS), (unsigned)((N + 31) / 32)), NT, 0, s,
+                 (const float *)nullptr, 0, M, N, g.e);
     }
-    if (own && prod) { dz = ws.p; ldz = lddz; }
-    if (gb) {
-      float *from = g.e.colpart, *to = from + (size_t)cr * N;
-      for (int P = crows;; std::swap(from, to)) {
-        const int q = (P + CROWS - 1) / CROWS;
-        E2F_LAUNCH(colsum_kernel, dim3((N + 31) / 32, q), 256, 0, s, from, P, N, q == 1 ? gb : to);
-        if ((P = q) == 1) break;
-      }
+    after = true;
+    if (prod) { dz = ws.p; ldz = lddz; }
+    cp = g.e.colpart; ctype = E2F_F32; cld = N;
+  }
+  if (gb) {
+    float *to = reinterpret_cast<float *>(ws.as<char>() + zb) + (size_t)cr * N, *other = to + (size_t)cr2 * N;
+    for (;;) {
+      const int q = (crows + CROWS - 1) / CROWS;
+      const dim3 grid((unsigned)((N + 31) / 32), (unsigned)q);
+      if (after) E2F_LAUNCH_AFTER(colsum_kernel, grid, 1024, 0, s, cp, ctype, cld, crows, N, q == 1 ? gb : to);
+      else E2F_LAUNCH(colsum_kernel, grid, 1024, 0, s, cp, ctype, cld, crows, N, q == 1 ? gb : to);
+      after = true;
+      if (q == 1) break;
+      cp = to; ctype = E2F_F32; cld = N; crows = q;
+      std::swap(to, other);
     }
   }
   if (gx) {
     Gemm g{};
     g.A = dz; g.lda = ldz; g.B = p.W; g.ldb = p.ldw;
     g.M = M; g.N = K; g.K = N;
+    g.after = after;
+    after = true;
     g.e.mode = MODE_OUT; g.e.act = E2F_ACT_NONE;
     g.e.out = gx; g.e.ldo = ldgx; g.e.otype = TT;
     e2f_status st = run_gemm<T, false, true>(g, s);
@@ -258,6 +281,7 @@ static e2f_status backward(const e2f_linear &p, const void *dy, int64_t ldg, int
     Gemm g{};
     g.A = dz; g.lda = ldz; g.B = p.x; g.ldb = p.ldx;
     g.M = N; g.N = K; g.K = M;
+    g.after = after;
     g.e.mode = MODE_OUT; g.e.act = E2F_ACT_NONE;
     g.e.out = gW; g.e.ldo = ldgw; g.e.otype = TT;
     e2f_status st = run_gemm<T, true, true>(g, s);

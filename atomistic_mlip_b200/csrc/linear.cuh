@@ -5,6 +5,13 @@
 #include "common.cuh"
 #include "tc_common.cuh"
 
+// Launch by g.after: behind another kernel of the call, or in plain stream order.
+#define E2F_LIN_LAUNCH(g, kernel, grid, block, smem, stream, ...)              \
+  do {                                                                         \
+    if ((g).after) E2F_LAUNCH_AFTER(kernel, grid, block, smem, stream, __VA_ARGS__); \
+    else E2F_LAUNCH(kernel, grid, block, smem, stream, __VA_ARGS__);           \
+  } while (0)
+
 namespace e2f {
 namespace lin {
 
@@ -33,6 +40,7 @@ struct Gemm {
   int M, N, K;
   int kper;          // contraction blocks (of BK) per split
   float *part;       // MODE_PART
+  bool after;        // launched behind another kernel of the call
   Epi e;
 };
 

@@ -170,6 +170,7 @@ __global__ void __launch_bounds__(NT, 1) gemm_reg_kernel(const __grid_constant__
   tc_fence_after();
   const uint32_t tmem = tslot;
   const Gemm &g = a.g;
+  after_previous();
 
   if (warp < CTRL_WARP) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
@@ -351,11 +352,11 @@ static e2f_status launch(const Args &a, int sms, cudaStream_t s) {
   if (long_chain(a.g)) {
     constexpr auto k = gemm_reg_kernel<T, AMN, BMN, EPI, true>;
     E2F_CUDA_TRY(allow_smem<k>(smem_bytes<T>(), LAUNCH_REGS));
-    E2F_LAUNCH(k, std::min(a.s.tiles, sms), NT, smem_bytes<T>(), s, a);
+    E2F_LIN_LAUNCH(a.g, k, std::min(a.s.tiles, sms), NT, smem_bytes<T>(), s, a);
   } else {
     constexpr auto k = gemm_reg_kernel<T, AMN, BMN, EPI, false>;
     E2F_CUDA_TRY(allow_smem<k>(smem_bytes<T>(), LAUNCH_REGS));
-    E2F_LAUNCH(k, std::min(a.s.tiles, sms), NT, smem_bytes<T>(), s, a);
+    E2F_LIN_LAUNCH(a.g, k, std::min(a.s.tiles, sms), NT, smem_bytes<T>(), s, a);
   }
   return E2F_OK;
 }

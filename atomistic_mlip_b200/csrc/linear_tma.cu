@@ -94,6 +94,7 @@ gemm_tma_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ 
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tslot;
+  after_previous();
 
   // LONGK: the register sums need more than the 168 that 384 threads are
   // launched with: 40 + 2 * 232 = 3 * 168.
@@ -276,7 +277,7 @@ template <bool AMN, bool BMN, int BN, bool LONGK, int EPI, int EW>
 static e2f_status launch_epi(const CUtensorMap &ta, const CUtensorMap &tb, const Args &a, int sms, cudaStream_t s) {
   constexpr auto k = gemm_tma_kernel<AMN, BMN, BN, LONGK, EPI, EW>;
   E2F_CUDA_TRY(allow_smem<k>(smem_bytes<EW>(), LONGK ? 168 : 0));
-  E2F_LAUNCH(k, std::min(a.s.tiles, sms), threads<EW>(), smem_bytes<EW>(), s, ta, tb, a);
+  E2F_LIN_LAUNCH(a.g, k, std::min(a.s.tiles, sms), threads<EW>(), smem_bytes<EW>(), s, ta, tb, a);
   return E2F_OK;
 }
 

@@ -379,60 +379,58 @@ def attention_backward(x, pos, nl: NeighborList, w: DeviceWeights, grad_out, str
 # ----------------------------------------------------------------------------
 # the two ends of a model
 # ----------------------------------------------------------------------------
-_CODES = {}
+_FLOAT, _ID = {}, {}   # tensor type -> type code of the C ABI
 
 
-def _code(t, what: str, kinds: str) -> int:
-    """Type code of a tensor for the C ABI; `kinds` 'f' (float32, bfloat16) or
-    'i' (int32, int64)."""
-    if not _CODES:
-        torch = _torch()
-        _CODES.update({("f", torch.float32): F32, ("f", torch.bfloat16): BF16, ("i", torch.int32): I32,
-                       ("i", torch.int64): I64})
-    code = _CODES.get((kinds, t.dtype))
+def _types():
+    torch = _torch()
+    _FLOAT.update({torch.float32: F32, torch.bfloat16: BF16})
+    _ID.update({torch.int32: I32, torch.int64: I64})
+
+
+def _float_code(t, what: str) -> int:
+    if not _FLOAT:
+        _types()
+    code = _FLOAT.get(t.dtype)
     if code is None:
-        raise ValueError(f"{what} has type {t.dtype}")
+        raise ValueError(f"{what} has type {t.dtype}, expected float32 or bfloat16")
     return code
 
 
-def _same_device(**tensors) -> int:
-    """Index of the one CUDA device that holds the tensors."""
-    first = dev = None
-    for name, t in tensors.items():
-        if t is None:
-            continue
-        d = t.get_device()
-        if d < 0:
-            raise ValueError(f"{name} is not on a CUDA device")
-        if dev is None:
-            first, dev = name, d
-        elif d != dev:
-            raise ValueError(f"{name} is on device {d}, {first} on device {dev}")
-    return dev
+def _id_code(ids) -> int:
+    if not _ID:
+        _types()
+    code = _ID.get(ids.dtype)
+    if code is None:
+        raise ValueError(f"ids have type {ids.dtype}, expected int32 or int64")
+    return code
 
 
-def _call(dev: int, stream, fn: str, *args):
-    """A library call on device `dev` (made the current one while it runs) and
-    on `stream`, or that device's current stream."""
+def _call(fn: str, stream, tensors, *args):
+    """A library call on the one CUDA device that holds the tensors (made the
+    current one while the call runs) and on `stream`, or that device's current
+    stream."""
     torch = _torch()
+    dev = tensors[0].get_device()
+    for t in tensors:
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"{fn}: tensors on several devices")
+    if dev < 0:
+        raise ValueError(f"{fn}: tensors are not on a CUDA device")
     if stream is None:
         s = torch._C._cuda_getCurrentRawStream(dev)
     elif stream.device_index != dev:
-        raise ValueError(f"the stream is on device {stream.device_index}, the tensors on device {dev}")
+        raise ValueError(f"{fn}: the stream is on device {stream.device_index}, the tensors on device {dev}")
     else:
         s = stream.cuda_stream
+    f = getattr(_lib or lib(), fn)
     if torch.cuda.current_device() == dev:
-        code = getattr(lib(), fn)(*args, s)
+        code = f(*args, s)
     else:
         with torch.cuda.device(dev):
-            code = getattr(lib(), fn)(*args, s)
+            code = f(*args, s)
     if code:
         _check(code, fn)
-
-
-def _need(cond, msg: str):
-    if not cond:
-        raise ValueError(msg)
 
 
 def embed_forward(ids, table, scale: float = 1.0, Q: int = 1, out_dtype=None, out=None, stream=None):
@@ -442,17 +440,18 @@ def embed_forward(ids, table, scale: float = 1.0, Q: int = 1, out_dtype=None, ou
     given.  An id outside the table gives zeros and is reported by
     stream_status()."""
     torch = _torch()
-    _need(ids.dim() == 1 and ids.is_contiguous(), "ids must be a contiguous vector")
-    _need(table.dim() == 2 and table.is_contiguous(), "table must be contiguous [V, D]")
-    N, (V, D) = int(ids.shape[0]), table.shape
-    it, tt = _code(ids, "ids", "i"), _code(table, "table", "f")
+    if ids.dim() != 1 or not ids.is_contiguous():
+        raise ValueError("ids must be a contiguous vector")
+    if table.dim() != 2 or not table.is_contiguous():
+        raise ValueError("table must be contiguous [V, D]")
+    N, (V, D) = ids.shape[0], table.shape
+    it, tt = _id_code(ids), _float_code(table, "table")
     if out is None:
-        out = torch.empty((N, Q, D), dtype=out_dtype or torch.float32, device=table.device)
-    else:
-        _need(out.shape == (N, Q, D) and out.is_contiguous(), f"out must be contiguous {(N, Q, D)}")
-        _need(out_dtype is None or out.dtype == out_dtype, "out has another type than out_dtype")
-    _call(_same_device(ids=ids, table=table, out=out), stream, "e2f_embed_forward", ids.data_ptr(), it, N,
-          table.data_ptr(), tt, V, D, scale, Q, out.data_ptr(), _code(out, "out", "f"))
+        out = table.new_empty((N, Q, D), dtype=out_dtype or torch.float32)
+    elif out.shape != (N, Q, D) or not out.is_contiguous() or (out_dtype is not None and out.dtype != out_dtype):
+        raise ValueError(f"out must be contiguous {(N, Q, D)}, of out_dtype if that is given")
+    _call("e2f_embed_forward", stream, (ids, table, out), ids.data_ptr(), it, N, table.data_ptr(), tt, V, D, scale, Q,
+          out.data_ptr(), _float_code(out, "out"))
     return out
 
 
@@ -462,20 +461,21 @@ def embed_backward(ids, grad_out, V: int, scale: float = 1.0, grad_table=None, a
     rows of each id.  With accumulate the sums are added to grad_table.  Sums
     in a fixed order: the result repeats bit for bit."""
     torch = _torch()
-    _need(ids.dim() == 1 and ids.is_contiguous(), "ids must be a contiguous vector")
-    _need(grad_out.dim() in (2, 3) and grad_out.is_contiguous(), "grad_out must be contiguous [N, Q, D] or [N, D]")
-    N, D = int(ids.shape[0]), int(grad_out.shape[-1])
-    _need(int(grad_out.shape[0]) == N, f"grad_out has {int(grad_out.shape[0])} rows, ids {N}")
-    Q = int(grad_out.shape[1]) if grad_out.dim() == 3 else 1
-    it, gt = _code(ids, "ids", "i"), _code(grad_out, "grad_out", "f")
+    if ids.dim() != 1 or not ids.is_contiguous():
+        raise ValueError("ids must be a contiguous vector")
+    if grad_out.dim() not in (2, 3) or not grad_out.is_contiguous() or grad_out.shape[0] != ids.shape[0]:
+        raise ValueError("grad_out must be contiguous [N, Q, D] or [N, D], N the number of ids")
+    N, D = ids.shape[0], grad_out.shape[-1]
+    Q = grad_out.shape[1] if grad_out.dim() == 3 else 1
+    it, gt = _id_code(ids), _float_code(grad_out, "grad_out")
     if grad_table is None:
-        _need(not accumulate, "accumulate needs grad_table")
-        grad_table = torch.empty((V, D), dtype=torch.float32, device=grad_out.device)
-    else:
-        _need(grad_table.shape == (V, D) and grad_table.is_contiguous() and grad_table.dtype == torch.float32,
-              f"grad_table must be contiguous float32 {(V, D)}")
-    _call(_same_device(ids=ids, grad_out=grad_out, grad_table=grad_table), stream, "e2f_embed_backward",
-          ids.data_ptr(), it, N, grad_out.data_ptr(), gt, V, D, scale, Q, grad_table.data_ptr(), int(bool(accumulate)))
+        if accumulate:
+            raise ValueError("accumulate needs grad_table")
+        grad_table = grad_out.new_empty((V, D), dtype=torch.float32)
+    elif grad_table.shape != (V, D) or not grad_table.is_contiguous() or grad_table.dtype != torch.float32:
+        raise ValueError(f"grad_table must be contiguous float32 {(V, D)}")
+    _call("e2f_embed_backward", stream, (ids, grad_out, grad_table), ids.data_ptr(), it, N, grad_out.data_ptr(), gt, V,
+          D, scale, Q, grad_table.data_ptr(), 1 if accumulate else 0)
     return grad_table
 
 
@@ -497,16 +497,20 @@ def _ld(t, rows: int, cols: int, what: str) -> int:
 
 
 def _linear_struct(x, W, bias, act: str):
-    _need(x.dim() == 2 and W.dim() == 2, "x and W must be [M, K] and [N, K]")
-    M, (N, K) = int(x.shape[0]), W.shape
-    code = _code(x, "x", "f")
-    _need(W.dtype == x.dtype, f"W has type {W.dtype}, x {x.dtype}")
-    _need(act in ACT, f"act must be one of {sorted(ACT)}")
+    if x.dim() != 2 or W.dim() != 2:
+        raise ValueError("x and W must be [M, K] and [N, K]")
+    M, (N, K) = x.shape[0], W.shape
+    code = _float_code(x, "x")
+    if W.dtype != x.dtype:
+        raise ValueError(f"W has type {W.dtype}, x {x.dtype}")
+    if act not in ACT:
+        raise ValueError(f"act must be one of {sorted(ACT)}")
+    bp = None
     if bias is not None:
-        _need(bias.dtype == _torch().float32 and bias.shape == (N,) and bias.is_contiguous(),
-              f"bias must be contiguous float32 [{N}]")
-    return Linear(code, ACT[act], M, K, N, x.data_ptr(), _ld(x, M, K, "x"), W.data_ptr(), _ld(W, N, K, "W"),
-                  None if bias is None else bias.data_ptr()), M, K, N
+        if bias.dtype != _torch().float32 or bias.shape != (N,) or not bias.is_contiguous():
+            raise ValueError(f"bias must be contiguous float32 [{N}]")
+        bp = bias.data_ptr()
+    return Linear(code, ACT[act], M, K, N, x.data_ptr(), _ld(x, M, K, "x"), W.data_ptr(), _ld(W, N, K, "W"), bp), M, K, N
 
 
 def linear_forward(x, W, bias=None, residual=None, act: str = "none", out=None, out_dtype=None, stream=None):
@@ -514,18 +518,18 @@ def linear_forward(x, W, bias=None, residual=None, act: str = "none", out=None, 
     bfloat16 with any row stride (x may be features[:, 0] of [M, Q, K]), bias
     float32 [N], act "none", "silu" or "gelu"; residual has the output's type
     (x's unless given by out_dtype or out) and may be out itself."""
-    torch = _torch()
     p, M, K, N = _linear_struct(x, W, bias, act)
     if out is None:
-        out = torch.empty((M, N), dtype=out_dtype or x.dtype, device=x.device)
-    else:
-        _need(out_dtype is None or out.dtype == out_dtype, "out has another type than out_dtype")
+        out = x.new_empty((M, N), dtype=out_dtype)
+    elif out_dtype is not None and out.dtype != out_dtype:
+        raise ValueError("out has another type than out_dtype")
     ldo, ldr = _ld(out, M, N, "out"), N
     if residual is not None:
         ldr = _ld(residual, M, N, "residual")
-        _need(residual.dtype == out.dtype, f"residual has type {residual.dtype}, the output {out.dtype}")
-    _call(_same_device(x=x, W=W, bias=bias, residual=residual, out=out), stream, "e2f_linear_forward",
-          ctypes.byref(p), _ptr(residual), ldr, out.data_ptr(), ldo, _code(out, "out", "f"))
+        if residual.dtype != out.dtype:
+            raise ValueError(f"residual has type {residual.dtype}, the output {out.dtype}")
+    _call("e2f_linear_forward", stream, (x, W, bias, residual, out), ctypes.byref(p), _ptr(residual), ldr,
+          out.data_ptr(), ldo, _float_code(out, "out"))
     return out
 
 
@@ -541,21 +545,22 @@ def linear_backward(x, W, grad_out, bias=None, act: str = "none", need_x: bool =
     ldg = _ld(grad_out, M, N, "grad_out")
     if need_bias is None:
         need_bias = bias is not None
-    gb = torch.empty((N,), dtype=torch.float32, device=x.device) if need_bias else None
-    if grad_x is None and need_x:
-        grad_x = torch.empty((M, K), dtype=x.dtype, device=x.device)
-    if grad_W is None and need_W:
-        grad_W = torch.empty((N, K), dtype=x.dtype, device=x.device)
+    gb = x.new_empty((N,), dtype=torch.float32) if need_bias else None
     ldgx = ldgw = K
     if grad_x is not None:
         ldgx = _ld(grad_x, M, K, "grad_x")
-        _need(grad_x.dtype == x.dtype, f"grad_x has type {grad_x.dtype}, x {x.dtype}")
+        if grad_x.dtype != x.dtype:
+            raise ValueError(f"grad_x has type {grad_x.dtype}, x {x.dtype}")
+    elif need_x:
+        grad_x = x.new_empty((M, K))
     if grad_W is not None:
         ldgw = _ld(grad_W, N, K, "grad_W")
-        _need(grad_W.dtype == x.dtype, f"grad_W has type {grad_W.dtype}, x {x.dtype}")
-    _call(_same_device(x=x, W=W, bias=bias, grad_out=grad_out, grad_x=grad_x, grad_W=grad_W), stream,
-          "e2f_linear_backward", ctypes.byref(p), grad_out.data_ptr(), ldg, _code(grad_out, "grad_out", "f"),
-          _ptr(grad_x), ldgx, _ptr(grad_W), ldgw, _ptr(gb))
+        if grad_W.dtype != x.dtype:
+            raise ValueError(f"grad_W has type {grad_W.dtype}, x {x.dtype}")
+    elif need_W:
+        grad_W = x.new_empty((N, K))
+    _call("e2f_linear_backward", stream, (x, W, bias, grad_out, grad_x, grad_W), ctypes.byref(p), grad_out.data_ptr(),
+          ldg, _float_code(grad_out, "grad_out"), _ptr(grad_x), ldgx, _ptr(grad_W), ldgw, _ptr(gb))
     return grad_x, grad_W, gb
 
 
