@@ -564,6 +564,71 @@ def linear_backward(x, W, grad_out, bias=None, act: str = "none", need_x: bool =
     return grad_x, grad_W, gb
 
 
+class DeviceReadout:
+    """Readout of per-atom energies from the invariant features, float32 on the
+    device: e_n = W2 SiLU(W1 x[n, (0, 0)] + b1) + b2, W1 [Hr, C], b1 [Hr],
+    W2 [1, Hr], b2 [1]."""
+
+    def __init__(self, W1, b1, W2, b2):
+        self.W1, self.b1, self.W2, self.b2 = W1, b1, W2, b2
+
+
+def readout_forward(x, head: DeviceReadout, stream=None):
+    """(per-atom energies [N, 1], hidden features [N, Hr]) of the residual
+    stream or attention output x (float32 [N, Q, C])."""
+    h = linear_forward(x[:, 0], head.W1, bias=head.b1, act="silu", stream=stream)
+    return linear_forward(h, head.W2, bias=head.b2, stream=stream), h
+
+
+def readout_backward(x, h, grad_e, head: DeviceReadout, stream=None):
+    """Gradients of sum(grad_e * e): (dL/dx [N, Q, C], zero for l > 0, and a
+    dict of those of W1, b1, W2, b2); h from readout_forward."""
+    torch = _torch()
+    gh, gW2, gb2 = linear_backward(h, head.W2, grad_e, bias=head.b2, stream=stream)
+    with torch.cuda.stream(stream):   # None: the current stream
+        gx = torch.zeros_like(x)
+    _, gW1, gb1 = linear_backward(x[:, 0], head.W1, gh, bias=head.b1, act="silu", grad_x=gx[:, 0], stream=stream)
+    return gx, dict(W1=gW1, b1=gb1, W2=gW2, b2=gb2)
+
+
+def structure_sum(values, structure, n_structures: int, stream=None):
+    """Sums [n_structures] of per-atom values [N, 1] by the structure index of
+    every atom (-1: the atom takes no part)."""
+    return embed_backward(structure, values, n_structures, stream=stream)[:, 0]
+
+
+def model_energy(species, pos, nl: NeighborList, table, layers: List[DeviceBlockWeights], head: DeviceReadout, structure,
+                 n_structures: int, scale: float = 1.0, stream=None):
+    """Energies [n_structures] from species: scaled embedding -> blocks ->
+    readout -> sum over the atoms of each structure.  table float32 [V, C]."""
+    Q = (layers[0].attn.L + 1) ** 2
+    x = embed_forward(species, table, scale=scale, Q=Q, stream=stream)
+    e, _ = readout_forward(model_forward(x, pos, nl, layers, stream=stream), head, stream=stream)
+    return structure_sum(e, structure, n_structures, stream=stream)
+
+
+def attention_energy_forces(species, pos, nl: NeighborList, table, w: DeviceWeights, head: DeviceReadout, structure,
+                            n_structures: int, scale: float = 1.0, grad_energy=None, stream=None):
+    """Energies, conservative forces and training gradients of the model
+    species -> scaled embedding -> attention -> readout -> structure sums.
+
+    Returns (energies [n_structures], forces [N, 3], gradients: "table", "W1",
+    "b1", "W2", "b2"); the last two are those of sum(grad_energy * energies)
+    (grad_energy float32 [n_structures], ones unless given)."""
+    torch = _torch()
+    x = embed_forward(species, table, scale=scale, Q=(w.L + 1) ** 2, out_dtype=w.torch_dtype, stream=stream)
+    o = attention_forward(x, pos, nl, w, stream=stream)
+    e, h = readout_forward(o, head, stream=stream)
+    energies = structure_sum(e, structure, n_structures, stream=stream)
+    with torch.cuda.stream(stream):
+        gE = torch.ones_like(energies) if grad_energy is None else grad_energy
+    ge = embed_forward(structure, gE.view(n_structures, 1), stream=stream)[:, :, 0]   # every atom its structure's
+    go, grads = readout_backward(o, h, ge, head, stream=stream)
+    gx, gp = attention_backward(x, pos, nl, w, go, stream=stream)
+    grads["table"] = embed_backward(species, gx, table.shape[0], scale=scale, stream=stream)
+    return energies, gp.neg_(), grads
+
+
 def project_qkv(x, w: DeviceWeights, stream=None):
     torch = _torch()
     q, k, v = (torch.empty_like(x) for _ in range(3))
