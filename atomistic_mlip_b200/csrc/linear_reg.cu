@@ -308,7 +308,7 @@ __global__ void __launch_bounds__(NT, 1) gemm_reg_kernel(const __grid_constant__
                            [&](int h, float (&v)[16]) {
           if constexpr (LONGK) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) v[j] = c ? acc[32 + 16 * h + j] : acc[16 * h + j];
+            for (int j = 0; j < 16; ++j) v[j] = acc[16 * h + j];
           } else {
             const uint32_t ta = tq + (u & 1) * ACC + cc + 16 * h;
             tmem_ld_32x32b_x16(ta, v);
@@ -332,6 +332,10 @@ __global__ void __launch_bounds__(NT, 1) gemm_reg_kernel(const __grid_constant__
             __syncwarp();
           }
         });
+        if constexpr (LONGK) {   // the next chunk's sums to the front: no index that depends on c
+#pragma unroll
+          for (int j = 0; j < 32; ++j) acc[j] = acc[j + 32];
+        }
       }
       if (!LONGK) {
         tc_fence_before();

@@ -216,11 +216,7 @@ gemm_tma_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ 
         epi_chunk<EPI, PW>(a.g, a.s.vec, t.split, rw, n, b, x, st, sbias, lane, [&](int h, float (&v)[PW]) {
           if constexpr (LONGK) {
 #pragma unroll
-            for (int k = 0; k < NCH; ++k)
-              if (k == c) {
-#pragma unroll
-                for (int j = 0; j < PW; ++j) v[j] = acc[32 * k + PW * h + j];
-              }
+            for (int j = 0; j < PW; ++j) v[j] = acc[PW * h + j];
           } else if constexpr (PW == 32) {
             tmem_ld_32x32b_x32(tq + (u & 1) * BN + 32 * c, v);
           } else {
@@ -228,6 +224,10 @@ gemm_tma_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ 
           }
         });
         if (AHEAD && more) x = nx;
+        if constexpr (LONGK) {   // the next chunk's sums to the front: no index that depends on c
+#pragma unroll
+          for (int j = 0; j + 32 < BW; ++j) acc[j] = acc[j + 32];
+        }
       }
       if (!LONGK) {
         tc_fence_before();
