@@ -22,7 +22,8 @@ namespace lin {
 
 // linear_tma.cu
 bool tma_operand(const void *p, long long ld);
-template <bool AMN, bool BMN> e2f_status gemm_tma(const Gemm &g, int splits, int bn, int sms, cudaStream_t s);
+template <bool AMN, bool BMN>
+e2f_status gemm_tma(const Gemm &g, int splits, int bn, int sms, cudaStream_t s, int *rows_out);
 
 // linear_reg.cu
 template <typename T, bool AMN, bool BMN> e2f_status gemm_reg(const Gemm &g, int splits, int bn, int sms, cudaStream_t s);
@@ -128,17 +129,18 @@ static int sm_count() {   // one kind of device
   return n;
 }
 
-// Row blocks of 32 whose column sums a MODE_DZ product leaves.
-static int64_t colpart_rows(int64_t M) { return (M + FROWS - 1) / FROWS; }
+// Partial rows of column sums that a MODE_DZ product leaves at most: one of 32
+// rows, or four of a 128-row tile.
+static int64_t colpart_rows(int64_t M) { return 4 * ((M + BM - 1) / BM); }
 
 template <typename T, bool AMN, bool BMN> struct Path {
   static bool tma(const Gemm &) { return false; }
-  static e2f_status run_tma(const Gemm &, int, int, int, cudaStream_t) { return E2F_ERR_UNSUPPORTED; }
+  static e2f_status run_tma(const Gemm &, int, int, int, cudaStream_t, int *) { return E2F_ERR_UNSUPPORTED; }
 };
 template <bool AMN, bool BMN> struct Path<__nv_bfloat16, AMN, BMN> {
   static bool tma(const Gemm &g) { return tma_operand(g.A, g.lda) && tma_operand(g.B, g.ldb); }
-  static e2f_status run_tma(const Gemm &g, int splits, int bn, int sms, cudaStream_t s) {
-    return gemm_tma<AMN, BMN>(g, splits, bn, sms, s);
+  static e2f_status run_tma(const Gemm &g, int splits, int bn, int sms, cudaStream_t s, int *rows_out) {
+    return gemm_tma<AMN, BMN>(g, splits, bn, sms, s, rows_out);
   }
 };
 
@@ -177,9 +179,9 @@ static e2f_status run_gemm(Gemm g, cudaStream_t s, int *rows_out = nullptr) {
     g.part = ws.as<float>();
     g.e.mode = MODE_PART;
   }
-  e2f_status st = tma ? Path<T, AMN, BMN>::run_tma(g, splits, bn, sms, s)
+  if (rows_out) *rows_out = (int)((g.M + 31) / 32);
+  e2f_status st = tma ? Path<T, AMN, BMN>::run_tma(g, splits, bn, sms, s, rows_out)
                       : gemm_reg<T, AMN, BMN>(g, splits, bn, sms, s);
-  if (rows_out) *rows_out = (int)colpart_rows(g.M);
   if (st != E2F_OK || splits == 1) return st;
   const unsigned fy = (unsigned)((g.N + 31) / 32);
   if (e.mode == MODE_OUT && splits > 8) {
@@ -240,7 +242,7 @@ static e2f_status backward(const e2f_linear &p, const void *dy, int64_t ldg, int
     g.e.extra = dy; g.e.lde = ldg; g.e.etype = out_dtype;
     g.e.out = prod ? ws.p : nullptr; g.e.ldo = lddz; g.e.otype = TT;
     g.e.colpart = gb ? reinterpret_cast<float *>(ws.as<char>() + zb) : nullptr;
-    crows = (int)cr;
+    crows = (int)((M + FROWS - 1) / FROWS);
     if (p.act != E2F_ACT_NONE) {
       e2f_status st = run_gemm<T, false, false>(g, s, &crows);
       if (st != E2F_OK) return st;

@@ -91,6 +91,69 @@ __device__ __forceinline__ float gelu_grad(float z) {
   const float p = normal_cdf(z, &e);
   return fmaf(0.39894228f * z, e, p);
 }
+// ---- two at a time: one issue slot for two fp32 operations (the epilogues are
+// bound by issue slots) -------------------------------------------------------------
+struct f2 {
+  float x, y;
+};
+__device__ __forceinline__ f2 add2(f2 a, f2 b) {
+  f2 r;
+  asm("{\n\t.reg .b64 p, q, s;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %5};\n\tadd.rn.f32x2 s, p, q;\n\t"
+      "mov.b64 {%0, %1}, s;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ f2 mul2(f2 a, f2 b) {
+  f2 r;
+  asm("{\n\t.reg .b64 p, q, s;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %5};\n\tmul.rn.f32x2 s, p, q;\n\t"
+      "mov.b64 {%0, %1}, s;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return r;
+}
+__device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
+  f2 r;
+  asm("{\n\t.reg .b64 p, q, t, s;\n\tmov.b64 p, {%2, %3};\n\tmov.b64 q, {%4, %5};\n\tmov.b64 t, {%6, %7};\n\t"
+      "fma.rn.f32x2 s, p, q, t;\n\tmov.b64 {%0, %1}, s;\n\t}"
+      : "=f"(r.x), "=f"(r.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return r;
+}
+__device__ __forceinline__ f2 both(float v) { return {v, v}; }
+__device__ __forceinline__ f2 sigmoid(f2 z) {
+  f2 e = mul2(z, both(-LOG2E));
+  e = add2({ex2f(e.x), ex2f(e.y)}, both(1.f));
+  return {rcpf(e.x), rcpf(e.y)};
+}
+__device__ __forceinline__ f2 silu(f2 z) { return mul2(z, sigmoid(z)); }
+__device__ __forceinline__ f2 silu_grad(f2 z) {
+  const f2 s = sigmoid(z);
+  return fma2(mul2(s, z), fma2(s, both(-1.f), both(1.f)), s);
+}
+__device__ __forceinline__ f2 normal_cdf(f2 z, f2 *e) {
+  f2 t = fma2({fabsf(z.x), fabsf(z.y)}, both(0.3275911f * 0.70710678f), both(1.f));
+  t = {rcpf(t.x), rcpf(t.y)};
+  f2 x = mul2(mul2(z, both(-0.5f * LOG2E)), z);
+  x = {ex2f(x.x), ex2f(x.y)};
+  f2 q = fma2(t, both(0.5f * 1.061405429f), both(0.5f * -1.453152027f));
+  q = fma2(q, t, both(0.5f * 1.421413741f));
+  q = fma2(q, t, both(0.5f * -0.284496736f));
+  q = fma2(q, t, both(0.5f * 0.254829592f));
+  q = fma2(mul2(q, t), mul2(x, both(-1.f)), both(0.5f));   // 1/2 - Phi(-|z|)
+  *e = x;
+  return add2({copysignf(q.x, z.x), copysignf(q.y, z.y)}, both(0.5f));
+}
+__device__ __forceinline__ f2 gelu(f2 z) {
+  f2 e;
+  return mul2(z, normal_cdf(z, &e));
+}
+__device__ __forceinline__ f2 gelu_grad(f2 z) {
+  f2 e;
+  const f2 p = normal_cdf(z, &e);
+  return fma2(mul2(z, both(0.39894228f)), e, p);
+}
+
 __device__ __forceinline__ float act_fwd(int act, float z) {
   return act == E2F_ACT_SILU ? silu(z) : act == E2F_ACT_GELU ? gelu(z) : z;
 }

@@ -20,6 +20,8 @@ constexpr int PLAIN = 0, ACT = 1, RES = 2, DZ = 3;
 struct Sched {
   int mt, nt, tiles, nkb, bn;   // tiles: mt * nt * splits
   int vec;                      // 16-byte rows of out and extra, N a multiple of 8
+  int fixed;                    // a CTA's tiles share their columns
+  int keep;                     // DZ: ... whose sums stay in registers
 };
 
 struct Tile {
@@ -46,78 +48,130 @@ struct Extra {   // 4 x 8 elements of residual or dL/dout: bf16 in lo, fp32 in l
   uint4 lo[4], hi[4];
 };
 
-__device__ __forceinline__ void unpack8(const uint4 &a, const uint4 &b, int type, float (&v)[8]) {
-  if (type == E2F_F32) {
-    v[0] = __uint_as_float(a.x); v[1] = __uint_as_float(a.y); v[2] = __uint_as_float(a.z); v[3] = __uint_as_float(a.w);
-    v[4] = __uint_as_float(b.x); v[5] = __uint_as_float(b.y); v[6] = __uint_as_float(b.z); v[7] = __uint_as_float(b.w);
+// Eight elements of type T (float, __nv_bfloat16) as four pairs, from the raw words.
+template <typename T> __device__ __forceinline__ void unpack8(const uint4 &a, const uint4 &b, f2 (&v)[4]) {
+  if constexpr (sizeof(T) == 4) {
+    v[0] = {__uint_as_float(a.x), __uint_as_float(a.y)};
+    v[1] = {__uint_as_float(a.z), __uint_as_float(a.w)};
+    v[2] = {__uint_as_float(b.x), __uint_as_float(b.y)};
+    v[3] = {__uint_as_float(b.z), __uint_as_float(b.w)};
   } else {
-    v[0] = __uint_as_float(a.x << 16); v[1] = __uint_as_float(a.x & 0xffff0000u);
-    v[2] = __uint_as_float(a.y << 16); v[3] = __uint_as_float(a.y & 0xffff0000u);
-    v[4] = __uint_as_float(a.z << 16); v[5] = __uint_as_float(a.z & 0xffff0000u);
-    v[6] = __uint_as_float(a.w << 16); v[7] = __uint_as_float(a.w & 0xffff0000u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t w = u4w(a, i);
+      v[i] = {__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u)};
+    }
   }
 }
-__device__ __forceinline__ void store8(void *p, int type, size_t i, const float (&v)[8]) {
-  if (type == E2F_F32) {
-    float4 *q = reinterpret_cast<float4 *>(static_cast<float *>(p) + i);
-    q[0] = make_float4(v[0], v[1], v[2], v[3]);
-    q[1] = make_float4(v[4], v[5], v[6], v[7]);
+template <typename T> __device__ __forceinline__ void store8(char *p, const f2 (&v)[4]) {
+  if constexpr (sizeof(T) == 4) {
+    reinterpret_cast<float4 *>(p)[0] = make_float4(v[0].x, v[0].y, v[1].x, v[1].y);
+    reinterpret_cast<float4 *>(p)[1] = make_float4(v[2].x, v[2].y, v[3].x, v[3].y);
   } else {
-    *reinterpret_cast<uint4 *>(static_cast<__nv_bfloat16 *>(p) + i) =
-        make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
+    *reinterpret_cast<uint4 *>(p) = make_uint4(pack_bf16x2(v[0].x, v[0].y), pack_bf16x2(v[1].x, v[1].y),
+                                               pack_bf16x2(v[2].x, v[2].y), pack_bf16x2(v[3].x, v[3].y));
   }
 }
 
 // A warp's 32 rows of a tile; lane l handles rows l / 4 + 8 q, q = 0 .. 3, eight
-// columns of each.
+// columns of each.  Addresses in bytes.
 struct Rows {
   int m0, n;                     // first row, rows that exist
-  size_t out, extra;             // offsets of row m0 + lane / 4
+  char *out;                     // row m0 + lane / 4 of the results (or partial sums)
+  const char *extra;
   long long ostep, xstep;        // eight rows on
 };
-__device__ __forceinline__ Rows rows_of(const Gemm &g, int m0, int lane) {
+__device__ __forceinline__ Rows rows_of(const Gemm &g, int split, int m0, int lane) {
   Rows r;
   r.m0 = m0;
   r.n = g.M - m0;
-  const long long ldo = g.e.mode == MODE_PART ? g.N : g.e.ldo, m = m0 + (lane >> 2);
-  r.out = (size_t)(m * ldo);
-  r.extra = (size_t)(m * g.e.lde);
-  r.ostep = 8 * ldo;
-  r.xstep = 8 * g.e.lde;
+  const long long m = m0 + (lane >> 2);
+  if (g.e.mode == MODE_PART) {
+    r.out = reinterpret_cast<char *>(g.part) + (((size_t)split * g.M + m) * g.N) * 4;
+    r.ostep = 32LL * g.N;
+  } else {
+    const int sz = g.e.otype == E2F_F32 ? 4 : 2;
+    r.out = static_cast<char *>(g.e.out) + (size_t)(m * g.e.ldo) * sz;
+    r.ostep = 8 * g.e.ldo * sz;
+  }
+  const int xz = g.e.etype == E2F_F32 ? 4 : 2;
+  r.extra = static_cast<const char *>(g.e.extra) + (size_t)(m * g.e.lde) * xz;
+  r.xstep = 8 * g.e.lde * xz;
   return r;
 }
 
 // The chunk's residual or dL/dout from column n on.
 __device__ __forceinline__ void load_extra(Extra &d, const Gemm &g, int vec, const Rows &rw, int n, int lane) {
-  const Epi &e = g.e;
-  const int ng = n + (lane & 3) * 8;
+  const int ng = n + (lane & 3) * 8, r8 = lane >> 2;
   if (!vec || ng >= g.N) return;
+  if (g.e.etype == E2F_F32) {
+    const char *p = rw.extra + 4 * (size_t)ng;
 #pragma unroll
-  for (int q = 0; q < 4; ++q) {
-    if (8 * q + (lane >> 2) < rw.n) {
-      const size_t o = rw.extra + (size_t)(q * rw.xstep) + ng;
-      if (e.etype == E2F_F32) {
-        const uint4 *p = reinterpret_cast<const uint4 *>(static_cast<const float *>(e.extra) + o);
-        d.lo[q] = p[0];
-        d.hi[q] = p[1];
-      } else {
-        d.lo[q] = *reinterpret_cast<const uint4 *>(static_cast<const __nv_bfloat16 *>(e.extra) + o);
+    for (int q = 0; q < 4; ++q, p += rw.xstep)
+      if (8 * q + r8 < rw.n) {
+        d.lo[q] = reinterpret_cast<const uint4 *>(p)[0];
+        d.hi[q] = reinterpret_cast<const uint4 *>(p)[1];
+      }
+  } else {
+    const char *p = rw.extra + 2 * (size_t)ng;
+#pragma unroll
+    for (int q = 0; q < 4; ++q, p += rw.xstep)
+      if (8 * q + r8 < rw.n) d.lo[q] = *reinterpret_cast<const uint4 *>(p);
+  }
+}
+
+// Column sums over a warp's rows: lane's eight columns of a chunk -> all rows
+// (lanes 4 apart hold the same columns), lanes 0 .. 3 write.
+__device__ __forceinline__ void flush_colsum(f2 (&cs)[4], float *row, int ng, int N, int lane) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+#pragma unroll
+    for (int o = 4; o < 32; o <<= 1)
+      cs[j] = add2(cs[j], {__shfl_xor_sync(0xffffffffu, cs[j].x, o), __shfl_xor_sync(0xffffffffu, cs[j].y, o)});
+  }
+  if (lane < 4 && ng < N) store8<float>(reinterpret_cast<char *>(row + ng), cs);
+}
+
+// Rows of a chunk from fp32 staging to memory, with the residual or dL/dout.
+template <int EPI, typename XT, typename OT>
+__device__ __forceinline__ void put_rows(const Rows &rw, const Extra &x, const float *st, f2 (&cs)[4], bool store, int ng,
+                                         int N, int lane) {
+  const int r8 = lane >> 2, c4 = (lane & 3) * 2;
+  char *o = rw.out + sizeof(OT) * (size_t)ng;
+#pragma unroll
+  for (int q = 0; q < 4; ++q, o += rw.ostep) {
+    const int row = 8 * q + r8;
+    if (row >= rw.n || ng >= N) continue;
+    const float4 lo = *reinterpret_cast<const float4 *>(st + row * 32 + ((c4 ^ (row & 7)) << 2));
+    const float4 hi = *reinterpret_cast<const float4 *>(st + row * 32 + (((c4 + 1) ^ (row & 7)) << 2));
+    f2 r[4] = {{lo.x, lo.y}, {lo.z, lo.w}, {hi.x, hi.y}, {hi.z, hi.w}};
+    if constexpr (EPI >= RES) {
+      f2 y[4];
+      unpack8<XT>(x.lo[q], x.hi[q], y);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        r[j] = EPI == RES ? add2(r[j], y[j]) : mul2(r[j], y[j]);
+        if (EPI == DZ) cs[j] = add2(cs[j], r[j]);
       }
     }
+    if (store) store8<OT>(o, r);
   }
 }
 
 // Columns n .. n + 31 of the warp's rows.  get(h, v) gives lane l the PW
 // accumulators of row l from column n + PW h on; bias: that of column n + lane;
 // x: the chunk's extra (load_extra); st: 4 KB, sbias: 32 floats of the warp.
+// DZ: the lane's column sums are added to cs where that is kept across tiles
+// (keep), else go to their row of e.colpart.
 template <int EPI, int PW, class Get>
 __device__ __forceinline__ void epi_chunk(const Gemm &g, int vec, int split, const Rows &rw, int n, float bias,
-                                          const Extra &x, float *st, float *sbias, int lane, Get get) {
+                                          const Extra &x, f2 (&cs)[4], bool keep, float *st, float *sbias, int lane,
+                                          Get get) {
   constexpr bool EXTRA = EPI >= RES;
   const Epi &e = g.e;
   // results that need nothing more are rounded before they are staged
   const bool half_rows = EPI <= ACT && e.mode == MODE_OUT && e.otype == E2F_BF16;
-  const int r8 = lane >> 2, cg = (lane & 3) * 8, ng = n + cg, rows = rw.n;
+  const int r8 = lane >> 2, ng = n + (lane & 3) * 8;
   if (EPI != PLAIN) {
     sbias[lane] = bias;
     __syncwarp();
@@ -126,132 +180,112 @@ __device__ __forceinline__ void epi_chunk(const Gemm &g, int vec, int split, con
   uint4 *sh = reinterpret_cast<uint4 *>(st);
 #pragma unroll
   for (int h = 0; h < 32 / PW; ++h) {
-    float v[PW];
-    get(h, v);
+    f2 v[PW / 2];
+    {
+      float w[PW];
+      get(h, w);
+#pragma unroll
+      for (int j = 0; j < PW / 2; ++j) v[j] = {w[2 * j], w[2 * j + 1]};
+    }
     if (EPI != PLAIN) {
       if (e.bias) {
 #pragma unroll
         for (int j = 0; j < PW / 4; ++j) {
           const float4 b4 = *reinterpret_cast<const float4 *>(sbias + PW * h + 4 * j);
-          v[4 * j] += b4.x; v[4 * j + 1] += b4.y; v[4 * j + 2] += b4.z; v[4 * j + 3] += b4.w;
+          v[2 * j] = add2(v[2 * j], {b4.x, b4.y});
+          v[2 * j + 1] = add2(v[2 * j + 1], {b4.z, b4.w});
         }
       }
       if (EPI != DZ) {
         if (e.act == E2F_ACT_SILU) {
 #pragma unroll
-          for (int j = 0; j < PW; ++j) v[j] = silu(v[j]);
+          for (int j = 0; j < PW / 2; ++j) v[j] = silu(v[j]);
         } else if (e.act == E2F_ACT_GELU) {
 #pragma unroll
-          for (int j = 0; j < PW; ++j) v[j] = gelu(v[j]);
+          for (int j = 0; j < PW / 2; ++j) v[j] = gelu(v[j]);
         }
       } else if (e.act == E2F_ACT_SILU) {
 #pragma unroll
-        for (int j = 0; j < PW; ++j) v[j] = silu_grad(v[j]);
+        for (int j = 0; j < PW / 2; ++j) v[j] = silu_grad(v[j]);
       } else {
 #pragma unroll
-        for (int j = 0; j < PW; ++j) v[j] = gelu_grad(v[j]);
+        for (int j = 0; j < PW / 2; ++j) v[j] = gelu_grad(v[j]);
       }
     }
     if (half_rows) {   // bf16 results as they go out: half the shared-memory traffic
 #pragma unroll
       for (int j = 0; j < PW / 8; ++j)
         sh[lane * 4 + ((PW / 8 * h + j) ^ ((lane >> 1) & 3))] =
-            make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
-                       pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
+            make_uint4(pack_bf16x2(v[4 * j].x, v[4 * j].y), pack_bf16x2(v[4 * j + 1].x, v[4 * j + 1].y),
+                       pack_bf16x2(v[4 * j + 2].x, v[4 * j + 2].y), pack_bf16x2(v[4 * j + 3].x, v[4 * j + 3].y));
     } else {
 #pragma unroll
       for (int j = 0; j < PW / 4; ++j)
         *reinterpret_cast<float4 *>(st + lane * 32 + (((PW / 4 * h + j) ^ (lane & 7)) << 2)) =
-            make_float4(v[4 * j], v[4 * j + 1], v[4 * j + 2], v[4 * j + 3]);
+            make_float4(v[2 * j].x, v[2 * j].y, v[2 * j + 1].x, v[2 * j + 1].y);
     }
   }
   __syncwarp();
   if (half_rows) {
-    __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(e.out);
     if (vec) {
+      char *o = rw.out + 2 * (size_t)ng;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
+      for (int q = 0; q < 4; ++q, o += rw.ostep) {
         const int row = 8 * q + r8;
         const uint4 w = sh[row * 4 + ((lane & 3) ^ ((row >> 1) & 3))];
-        if (row < rows && ng < g.N) *reinterpret_cast<uint4 *>(out + rw.out + (size_t)(q * rw.ostep) + ng) = w;
+        if (row < rw.n && ng < g.N) *reinterpret_cast<uint4 *>(o) = w;
       }
     } else if (n + lane < g.N) {
       const __nv_bfloat16 *s2 = reinterpret_cast<const __nv_bfloat16 *>(st);
+      __nv_bfloat16 *out = static_cast<__nv_bfloat16 *>(e.out) + (size_t)(rw.m0 * e.ldo) + n + lane;
 #pragma unroll 8
-      for (int r = 0; r < 32; ++r)
-        if (rw.m0 + r < g.M)
-          out[(size_t)((rw.m0 + r) * e.ldo) + n + lane] = s2[r * 32 + (((lane >> 3) ^ ((r >> 1) & 3)) << 3) + (lane & 7)];
+      for (int r = 0; r < 32; ++r, out += e.ldo)
+        if (r < rw.n) *out = s2[r * 32 + (((lane >> 3) ^ ((r >> 1) & 3)) << 3) + (lane & 7)];
     }
-  } else {
+  } else if (vec) {
+    if (EPI == DZ && !keep) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) cs[j] = both(0.f);
+    }
+    const bool store = EPI != DZ || e.out, xf = e.etype == E2F_F32, of = e.mode == MODE_PART || e.otype == E2F_F32;
+    if constexpr (EPI == DZ) {
+      if (xf && of) put_rows<EPI, float, float>(rw, x, st, cs, store, ng, g.N, lane);
+      else if (xf) put_rows<EPI, float, __nv_bfloat16>(rw, x, st, cs, store, ng, g.N, lane);
+      else if (of) put_rows<EPI, __nv_bfloat16, float>(rw, x, st, cs, store, ng, g.N, lane);
+      else put_rows<EPI, __nv_bfloat16, __nv_bfloat16>(rw, x, st, cs, store, ng, g.N, lane);
+    } else {   // the residual has the results' type
+      if (of) put_rows<EPI, float, float>(rw, x, st, cs, store, ng, g.N, lane);
+      else put_rows<EPI, __nv_bfloat16, __nv_bfloat16>(rw, x, st, cs, store, ng, g.N, lane);
+    }
+    if (EPI == DZ && !keep && e.colpart) flush_colsum(cs, e.colpart + (size_t)(rw.m0 >> 5) * g.N, ng, g.N, lane);
+  } else if (n + lane < g.N) {   // any alignment: lane = column
+    const int nl = n + lane;
     float *part = EPI != PLAIN || e.mode != MODE_PART ? nullptr : g.part + (size_t)split * g.M * g.N;
-    if (vec) {
-      float cs[8];
+    float sum = 0.f;
+    for (int r0 = 0; r0 < 32 && r0 < rw.n; r0 += 8) {
+      float y[8];
+      if (EXTRA) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) cs[j] = 0.f;
-#pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int row = 8 * q + r8;
-        if (row < rows && ng < g.N) {
-          const float4 lo = *reinterpret_cast<const float4 *>(st + row * 32 + (((cg >> 2) ^ (row & 7)) << 2));
-          const float4 hi = *reinterpret_cast<const float4 *>(st + row * 32 + ((((cg >> 2) + 1) ^ (row & 7)) << 2));
-          float r[8] = {lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w};
-          if (part) {
-            store8(part, E2F_F32, rw.out + (size_t)(q * rw.ostep) + ng, r);
-            continue;
-          }
-          if (EXTRA) {
-            float y[8];
-            unpack8(x.lo[q], x.hi[q], e.etype, y);
-            if (EPI == RES) {
-#pragma unroll
-              for (int j = 0; j < 8; ++j) r[j] += y[j];
-            } else {
-#pragma unroll
-              for (int j = 0; j < 8; ++j) {
-                r[j] *= y[j];
-                cs[j] += r[j];
-              }
-            }
-          }
-          if (EPI != DZ || e.out) store8(e.out, e.otype, rw.out + (size_t)(q * rw.ostep) + ng, r);
-        }
+        for (int r = 0; r < 8; ++r)
+          y[r] = r0 + r < rw.n ? load_as(e.extra, e.etype, (size_t)((rw.m0 + r0 + r) * e.lde) + nl) : 0.f;
       }
-      if (EPI == DZ && e.colpart) {   // column sums of the warp's 32 rows
 #pragma unroll
-        for (int j = 0; j < 8; ++j) {
-#pragma unroll
-          for (int o = 4; o < 32; o <<= 1) cs[j] += __shfl_xor_sync(0xffffffffu, cs[j], o);
+      for (int r = 0; r < 8; ++r) {
+        const int row = r0 + r, m = rw.m0 + row;
+        if (row >= rw.n) break;
+        float w = st[row * 32 + ((((lane >> 2) ^ (row & 7)) << 2) | (lane & 3))];
+        if (part) {
+          part[(size_t)m * g.N + nl] = w;
+          continue;
         }
-        if (lane < 4 && ng < g.N) store8(e.colpart, E2F_F32, (size_t)(rw.m0 >> 5) * g.N + ng, cs);
-      }
-    } else if (n + lane < g.N) {   // any alignment: lane = column
-      const int nl = n + lane;
-      float cs = 0.f;
-      for (int r0 = 0; r0 < 32 && rw.m0 + r0 < g.M; r0 += 8) {
-        float y[8];
         if (EXTRA) {
-#pragma unroll
-          for (int r = 0; r < 8; ++r)
-            y[r] = rw.m0 + r0 + r < g.M ? load_as(e.extra, e.etype, (size_t)((rw.m0 + r0 + r) * e.lde) + nl) : 0.f;
+          w = EPI == RES ? w + y[r] : w * y[r];
+          sum += w;
         }
-#pragma unroll
-        for (int r = 0; r < 8; ++r) {
-          const int row = r0 + r, m = rw.m0 + row;
-          if (m >= g.M) break;
-          float w = st[row * 32 + ((((lane >> 2) ^ (row & 7)) << 2) | (lane & 3))];
-          if (part) {
-            part[(size_t)m * g.N + nl] = w;
-            continue;
-          }
-          if (EXTRA) {
-            w = EPI == RES ? w + y[r] : w * y[r];
-            cs += w;
-          }
-          if (EPI != DZ || e.out) store_as(e.out, e.otype, (size_t)(m * e.ldo) + nl, w);
-        }
+        if (EPI != DZ || e.out) store_as(e.out, e.otype, (size_t)(m * e.ldo) + nl, w);
       }
-      if (EPI == DZ && e.colpart) e.colpart[(size_t)(rw.m0 >> 5) * g.N + nl] = cs;
     }
+    if (EPI == DZ && e.colpart) e.colpart[(size_t)(rw.m0 >> 5) * g.N + nl] = sum;
   }
   __syncwarp();
 }

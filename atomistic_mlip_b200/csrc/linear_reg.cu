@@ -261,7 +261,7 @@ __global__ void __launch_bounds__(NT, 1) gemm_reg_kernel(const __grid_constant__
     for (int i = blockIdx.x; i < a.s.tiles && ok; i += gridDim.x) {
       const Tile t = tile_of(g, a.s, i);
       const int mw = t.m0 + 32 * quarter;
-      const Rows rw = rows_of(g, mw, lane);
+      const Rows rw = rows_of(g, t.split, mw, lane);
       float bias[2];
 #pragma unroll
       for (int c = 0; c < 2; ++c) {
@@ -303,8 +303,9 @@ __global__ void __launch_bounds__(NT, 1) gemm_reg_kernel(const __grid_constant__
         const int cc = 32 * (half + 2 * c), n = t.n0 + cc;
         if (cc >= a.s.bn || n >= g.N || mw >= g.M) break;
         Extra x;
+        f2 cs[4];
         if (EXTRA) load_extra(x, g, a.s.vec, rw, n, lane);
-        epi_chunk<EPI, 16>(g, a.s.vec, t.split, rw, n, c ? bias[1] : bias[0], x, st, sbias, lane,
+        epi_chunk<EPI, 16>(g, a.s.vec, t.split, rw, n, c ? bias[1] : bias[0], x, cs, false, st, sbias, lane,
                            [&](int h, float (&v)[16]) {
           if constexpr (LONGK) {
 #pragma unroll

@@ -26,7 +26,10 @@ namespace lin {
 namespace tma {
 
 constexpr int BM = 128, BK = 64;
-constexpr int SHORTK = 8;                        // blocks of 64: up to here 16 epilogue warps
+// Contractions of up to so many blocks of 64 get 16 epilogue warps: there the
+// epilogue is the longer part of a tile (4,099 x 1,000 -> 2,050, dz: 45 us
+// against 63; 65,536 x 768 -> 1,024 without an extra operand: 97 against 94).
+constexpr int short_k(int epi) { return epi >= RES ? 16 : 8; }
 
 // EW epilogue warps (8 or 16) behind the four of the control warpgroup; 16 take a quarter of the
 // columns each and leave less room for the ring.
@@ -35,14 +38,17 @@ template <int EW> constexpr int staging() { return EW * 32 * 32 * 4; }
 template <int EW> constexpr int sbias() { return EW * 32 * 4; }
 template <int EW> constexpr int ring() { return EW == 16 ? 147456 : 196608; }
 template <int BN> constexpr int stage_bytes() { return (BM + BN) * BK * 2; }
-template <int BN, int EW> constexpr int stages() { return ring<EW>() / stage_bytes<BN>(); }
 template <int EW> constexpr size_t smem_bytes() { return ring<EW>() + staging<EW>() + sbias<EW>() + 256 + 1024; }
 
 struct Args {
   Gemm g;
   Sched s;
+  int grid;    // CTAs
+  int bres;    // bytes of B held for the whole launch (every CTA has one column tile), or 0
+  int st;      // stages of the ring behind them
   int *err;
 };
+constexpr int MAX_ST = 12;
 
 __device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, int x, int y, uint64_t *bar) {
   asm volatile(
@@ -74,18 +80,25 @@ __global__ void __launch_bounds__(threads<EW>(), 1)
 gemm_tma_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tbm,
                 const __grid_constant__ Args a) {
   using namespace tc;
-  constexpr int ST = stages<BN, EW>(), RING = ring<EW>(), STAGING = staging<EW>(), SBIAS = sbias<EW>(), SB = stage_bytes<BN>(), ABYTES = BM * BK * 2;
+  constexpr int RING = ring<EW>(), STAGING = staging<EW>(), SBIAS = sbias<EW>(), ABYTES = BM * BK * 2, BBYTES = BN * BK * 2;
   constexpr uint32_t LIMIT = 1u << 26;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   float *staging = reinterpret_cast<float *>(smem + RING);
-  uint64_t *full = reinterpret_cast<uint64_t *>(smem + RING + STAGING + SBIAS), *empty = full + ST, *tfull = empty + ST,
-           *tempty = tfull + 2;
+  uint64_t *full = reinterpret_cast<uint64_t *>(smem + RING + STAGING + SBIAS), *empty = full + MAX_ST,
+           *tfull = empty + MAX_ST, *tempty = tfull + 2, *bfull = tempty + 2;
+  // (stage counts known to the compiler where B moves with A: the issuing thread
+  // is on the critical path there)
+  constexpr bool BRES = EW == 16;
+  const int bres = BRES ? a.bres : 0;
+  const int ST = BRES ? a.st : RING / (ABYTES + BBYTES), SB = bres ? ABYTES : ABYTES + BBYTES;
+  uint8_t *ringp = smem + bres;
   __shared__ uint32_t tslot;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     for (int i = 0; i < ST; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
     for (int i = 0; i < 2; ++i) { mbar_init(&tfull[i], 1); mbar_init(&tempty[i], EW); }
+    mbar_init(bfull, 1);
     mbar_fence_init();
   }
   __syncthreads();
@@ -104,14 +117,19 @@ gemm_tma_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ 
       int s = 0;
       uint32_t ph = 1;   // the first pass over the ring finds it empty
       bool ok = true;
+      if (bres) {
+        const Tile t = tile_of(a.g, a.s, blockIdx.x);
+        mbar_arrive_expect_tx(bfull, bres);
+        for (int kb = 0; kb < t.kb1; ++kb) load_slice<BMN, BN>(smem + kb * BBYTES, &tbm, t.n0, kb * BK, bfull);
+      }
       for (int i = blockIdx.x; i < a.s.tiles && ok; i += gridDim.x) {
         const Tile t = tile_of(a.g, a.s, i);
         for (int kb = t.kb0; kb < t.kb1; ++kb) {
           ok = mbar_wait(&empty[s], ph, LIMIT);
           if (!ok) break;
           mbar_arrive_expect_tx(&full[s], SB);
-          load_slice<AMN, BM>(smem + s * SB, &ta, t.m0, kb * BK, &full[s]);
-          load_slice<BMN, BN>(smem + s * SB + ABYTES, &tbm, t.n0, kb * BK, &full[s]);
+          load_slice<AMN, BM>(ringp + s * SB, &ta, t.m0, kb * BK, &full[s]);
+          if (!bres) load_slice<BMN, BN>(ringp + s * SB + ABYTES, &tbm, t.n0, kb * BK, &full[s]);
           if (++s == ST) { s = 0; ph ^= 1; }
         }
       }
@@ -121,7 +139,7 @@ gemm_tma_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ 
     if (lane == 0) {
       int s = 0, u = 0;   // ring slot, accumulator units issued
       uint32_t ph = 0;
-      bool ok = true;
+      bool ok = !bres || mbar_wait(bfull, 0, LIMIT);
       for (int i = blockIdx.x; i < a.s.tiles && ok; i += gridDim.x) {
         const Tile t = tile_of(a.g, a.s, i);
         const int nb = min(BN, (a.g.N - t.n0 + 15) & ~15);
@@ -136,7 +154,7 @@ gemm_tma_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ 
             ok = mbar_wait(&full[s], ph, LIMIT);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t a0 = smem_addr(smem + s * SB), b0 = a0 + ABYTES;
+            const uint32_t a0 = smem_addr(ringp + s * SB), b0 = bres ? smem_addr(smem + kb * BBYTES) : a0 + ABYTES;
 #pragma unroll
             for (int k = 0; k < BK; k += 16)
               mma_bf16_ss(acc, slice_desc<AMN>(a0, k), slice_desc<BMN>(b0, k), id, kb > kc || k > 0 ? 1u : 0u);
@@ -159,11 +177,18 @@ gemm_tma_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ 
     constexpr int NCH = BW / 32;   // 32-column chunks of this warp
     int u = 0, bias_of = -1;
     float bias[NCH];
+    f2 sums[EPI == DZ ? NCH : 1][4];
+    if (EPI == DZ) {
+#pragma unroll
+      for (int k = 0; k < NCH; ++k)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) sums[k][j] = both(0.f);
+    }
     bool ok = true;
     for (int i = blockIdx.x; i < a.s.tiles && ok; i += gridDim.x) {
       const Tile t = tile_of(a.g, a.s, i);
       const int nw = t.n0 + cols, mw = t.m0 + 32 * quarter;
-      const Rows rw = rows_of(a.g, mw, lane);
+      const Rows rw = rows_of(a.g, t.split, mw, lane);
       if (EPI != PLAIN && nw != bias_of) {   // a CTA's tiles mostly share their columns
         bias_of = nw;
 #pragma unroll
@@ -197,9 +222,30 @@ gemm_tma_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ 
         tc_fence_after();
       }
       if (!ok) break;
-      // Not unrolled: the chunk's code fits the instruction cache once.
+      // Not unrolled: the chunk's code fits the instruction cache once.  What a
+      // chunk keeps in registers is always at the front of its array, which
+      // turns by one chunk each time: an index that depends on c would put the
+      // arrays into memory.
+      auto turn = [&] {
+        const float b0 = bias[0];
+#pragma unroll
+        for (int k = 0; k + 1 < NCH; ++k) bias[k] = bias[k + 1];
+        bias[NCH - 1] = b0;
+        if constexpr (EPI == DZ) {
+          f2 s0[4];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) s0[j] = sums[0][j];
+#pragma unroll
+          for (int k = 0; k + 1 < NCH; ++k)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) sums[k][j] = sums[k + 1][j];
+#pragma unroll
+          for (int j = 0; j < 4; ++j) sums[NCH - 1][j] = s0[j];
+        }
+      };
+      int c = 0;
 #pragma unroll 1
-      for (int c = 0; c < NCH; ++c) {
+      for (; c < NCH; ++c) {
         const int n = nw + 32 * c;
         if (n >= a.g.N || mw >= a.g.M) break;
         const bool more = c + 1 < NCH && n + 32 < a.g.N;
@@ -208,12 +254,10 @@ gemm_tma_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ 
           if (!AHEAD) load_extra(x, a.g, a.s.vec, rw, n, lane);
           else if (more) load_extra(nx, a.g, a.s.vec, rw, n + 32, lane);
         }
-        float b = bias[0];
-#pragma unroll
-        for (int k = 1; k < NCH; ++k) b = k == c ? bias[k] : b;
         // (16 columns at a time where the extra's registers live beside them)
         constexpr int PW = EXTRA && EW == 16 ? 16 : 32;
-        epi_chunk<EPI, PW>(a.g, a.s.vec, t.split, rw, n, b, x, st, sbias, lane, [&](int h, float (&v)[PW]) {
+        epi_chunk<EPI, PW>(a.g, a.s.vec, t.split, rw, n, bias[0], x, sums[0], a.s.keep, st, sbias, lane,
+                           [&](int h, float (&v)[PW]) {
           if constexpr (LONGK) {
 #pragma unroll
             for (int j = 0; j < PW; ++j) v[j] = acc[PW * h + j];
@@ -224,17 +268,26 @@ gemm_tma_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ 
           }
         });
         if (AHEAD && more) x = nx;
-        if constexpr (LONGK) {   // the next chunk's sums to the front: no index that depends on c
+        turn();
+        if constexpr (LONGK) {
 #pragma unroll
           for (int j = 0; j + 32 < BW; ++j) acc[j] = acc[j + 32];
         }
       }
+      for (; c < NCH; ++c) turn();   // once around
       if (!LONGK) {
         tc_fence_before();
         __syncwarp();
         if (lane == 0) mbar_arrive(&tempty[u & 1]);
         ++u;
       }
+    }
+    if (EPI == DZ && a.s.keep && e.colpart) {   // row (CTA among those of its columns, quarter)
+      const int n0 = tile_of(a.g, a.s, blockIdx.x).n0 + cols;
+      float *row = a.g.e.colpart + (size_t)((int)blockIdx.x / a.s.nt * 4 + quarter) * a.g.N;
+#pragma unroll
+      for (int k = 0; k < NCH; ++k)
+        if (n0 + 32 * k < a.g.N) flush_colsum(sums[k], row, n0 + 32 * k + (lane & 3) * 8, a.g.N, lane);
     }
     if (!ok && lane == 0) atomicExch(a.err, E2F_ERR_TIMEOUT);
   }
@@ -274,22 +327,27 @@ static bool encode(CUtensorMap *m, const void *p, long long rows, long long cols
 }
 
 template <bool AMN, bool BMN, int BN, bool LONGK, int EPI, int EW>
-static e2f_status launch_epi(const CUtensorMap &ta, const CUtensorMap &tb, const Args &a, int sms, cudaStream_t s) {
+static e2f_status launch_epi(const CUtensorMap &ta, const CUtensorMap &tb, Args a, cudaStream_t s) {
+  // B stays in shared memory for the launch where every CTA has one column tile
+  // and three stages of A fit beside it (100,002 x 128 -> 512: two thirds of the
+  // L2 reads; the time is the epilogue's and stays).
+  const long long bres = (long long)a.s.nkb * BN * BK * 2, abytes = BM * BK * 2;
+  a.bres = EW == 16 && a.s.fixed && a.g.kper == a.s.nkb && bres + 3 * abytes <= ring<EW>() ? (int)bres : 0;
+  a.st = std::min<int>(MAX_ST, (ring<EW>() - a.bres) / (a.bres ? (int)abytes : stage_bytes<BN>()));
   constexpr auto k = gemm_tma_kernel<AMN, BMN, BN, LONGK, EPI, EW>;
   E2F_CUDA_TRY(allow_smem<k>(smem_bytes<EW>(), LONGK ? 168 : 0));
-  E2F_LIN_LAUNCH(a.g, k, std::min(a.s.tiles, sms), threads<EW>(), smem_bytes<EW>(), s, ta, tb, a);
+  E2F_LIN_LAUNCH(a.g, k, a.grid, threads<EW>(), smem_bytes<EW>(), s, ta, tb, a);
   return E2F_OK;
 }
 
 template <bool AMN, bool BMN, int BN, bool LONGK>
-static e2f_status launch(const CUtensorMap &ta, const CUtensorMap &tb, const Args &a, int sms, cudaStream_t s) {
+static e2f_status launch(const CUtensorMap &ta, const CUtensorMap &tb, const Args &a, cudaStream_t s) {
   const int kind = epi_kind(a.g.e);
-  // A short contraction leaves the epilogue as the longer part of a tile.
   constexpr int W = LONGK ? 8 : 16;
-  const bool wide = !LONGK && a.g.kper <= SHORTK;
+  const bool wide = !LONGK && a.g.kper <= short_k(kind);
 #define E2F_LIN_EPI(E)                                                                \
-  return wide ? launch_epi<AMN, BMN, BN, LONGK, E, W>(ta, tb, a, sms, s)              \
-              : launch_epi<AMN, BMN, BN, LONGK, E, 8>(ta, tb, a, sms, s)
+  return wide ? launch_epi<AMN, BMN, BN, LONGK, E, W>(ta, tb, a, s)              \
+              : launch_epi<AMN, BMN, BN, LONGK, E, 8>(ta, tb, a, s)
   if constexpr (!AMN && !BMN) {
     if (kind == DZ) E2F_LIN_EPI(DZ);
     if (kind == RES) E2F_LIN_EPI(RES);
@@ -308,13 +366,25 @@ bool tma_operand(const void *p, long long ld) {
 // A bf16 product of aligned operands, split into `splits` parts of g.kper
 // contraction blocks (MODE_PART when there are several); bn = 128 or 256.
 template <bool AMN, bool BMN>
-e2f_status gemm_tma(const Gemm &g, int splits, int bn, int sms, cudaStream_t s) {
+e2f_status gemm_tma(const Gemm &g, int splits, int bn, int sms, cudaStream_t s, int *rows_out) {
   using namespace tma;
   Args a{};
   a.g = g;
   if (!schedule(g, splits, bn, &a.s)) return E2F_ERR_UNSUPPORTED;
   a.err = device_error_flag();
   if (!a.err) return E2F_ERR_CUDA;
+  // A grid that is a multiple of the column tiles gives each CTA one of them
+  // (where that takes no further wave of tiles).
+  a.grid = std::min(a.s.tiles, sms);
+  const int even = a.s.nt <= 16 && splits == 1 ? a.grid / a.s.nt * a.s.nt : 0;
+  if (even > 0 && (a.s.tiles + even - 1) / even == (a.s.tiles + a.grid - 1) / a.grid) {
+    a.grid = even;
+    a.s.fixed = 1;
+    if (g.e.mode == MODE_DZ && a.s.vec) {
+      a.s.keep = 1;
+      if (rows_out) *rows_out = even / a.s.nt * 4;
+    }
+  }
   CUtensorMap ta, tb;
   const bool ok = (AMN ? encode(&ta, g.A, g.K, g.M, g.lda, 64) : encode(&ta, g.A, g.M, g.K, g.lda, BM)) &&
                   (BMN ? encode(&tb, g.B, g.K, g.N, g.ldb, 64) : encode(&tb, g.B, g.N, g.K, g.ldb, bn));
@@ -324,12 +394,12 @@ e2f_status gemm_tma(const Gemm &g, int splits, int bn, int sms, cudaStream_t s) 
   }
   const bool longk = long_chain(g);
   if (bn == 256)
-    return longk ? launch<AMN, BMN, 256, true>(ta, tb, a, sms, s) : launch<AMN, BMN, 256, false>(ta, tb, a, sms, s);
-  return longk ? launch<AMN, BMN, 128, true>(ta, tb, a, sms, s) : launch<AMN, BMN, 128, false>(ta, tb, a, sms, s);
+    return longk ? launch<AMN, BMN, 256, true>(ta, tb, a, s) : launch<AMN, BMN, 256, false>(ta, tb, a, s);
+  return longk ? launch<AMN, BMN, 128, true>(ta, tb, a, s) : launch<AMN, BMN, 128, false>(ta, tb, a, s);
 }
-template e2f_status gemm_tma<false, false>(const Gemm &, int, int, int, cudaStream_t);
-template e2f_status gemm_tma<false, true>(const Gemm &, int, int, int, cudaStream_t);
-template e2f_status gemm_tma<true, true>(const Gemm &, int, int, int, cudaStream_t);
+template e2f_status gemm_tma<false, false>(const Gemm &, int, int, int, cudaStream_t, int *);
+template e2f_status gemm_tma<false, true>(const Gemm &, int, int, int, cudaStream_t, int *);
+template e2f_status gemm_tma<true, true>(const Gemm &, int, int, int, cudaStream_t, int *);
 
 }  // namespace lin
 }  // namespace e2f
