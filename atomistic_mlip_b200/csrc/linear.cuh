@@ -121,6 +121,9 @@ __device__ __forceinline__ f2 fma2(f2 a, f2 b, f2 c) {
   return r;
 }
 __device__ __forceinline__ f2 both(float v) { return {v, v}; }
+// (One reciprocal for a pair, (1 / (d.x d.y)) d.y and the same by d.x, saves a
+// special-function instruction in four but needs a guard against d.x d.y = inf:
+// 100,002 x 128 -> 512 SiLU 47 us against 40.)
 __device__ __forceinline__ f2 sigmoid(f2 z) {
   f2 e = mul2(z, both(-LOG2E));
   e = add2({ex2f(e.x), ex2f(e.y)}, both(1.f));

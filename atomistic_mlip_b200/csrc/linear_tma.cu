@@ -23,6 +23,10 @@
 namespace e2f {
 namespace lin {
 
+bool tma_operand(const void *p, long long ld) {
+  return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)(ld * 2)) & 15) == 0;
+}
+
 namespace tma {
 
 constexpr int BM = 128, BK = 64;
@@ -75,18 +79,207 @@ template <bool MN> __device__ __forceinline__ uint64_t slice_desc(uint32_t saddr
   return tc::smem_desc(a, MN ? 8192 : 16, 1024) | (uint64_t)2 << 61;
 }
 
-template <bool AMN, bool BMN, int BN, bool LONGK, int EPI, int EW>
+// ---- the asynchronous epilogue (IO): bf16 results, and bf16 residual or dL/dout ----
+// The chunk of 32 x 32 stays with lane = row: the extra operand arrives in shared
+// memory by TMA, the lane reads its row of it, writes its row of the result over
+// it, and TMA takes that out.  Against turning the chunk through shared memory
+// this halves the LSU wavefronts, which bound short contractions (100,002 x 128 ->
+// 512: 80 % of their peak): per chunk 32 for the accumulators, 16 in, 16 out, 8
+// for the bias.  Rows of 64 bytes, 64-byte swizzle.
+constexpr int IO_BUF = 2048;
+template <int EPI> constexpr int io_bufs() { return EPI >= RES ? 3 : 2; }
+template <int EPI> constexpr int io_ring() { return EPI >= RES ? 126976 : 147456; }
+constexpr int IO_SBIAS = 16 * 64 * 4;
+template <int EPI> constexpr size_t io_smem() {
+  return io_ring<EPI>() + 16 * io_bufs<EPI>() * IO_BUF + IO_SBIAS + 256 + 16 * io_bufs<EPI>() * 8 + 1024;
+}
+
+__device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, const void *src, int x, int y) {
+  asm volatile(
+      "cp.async.bulk.tensor.2d.global.shared::cta.tile.bulk_group [%0, {%1, %2}], [%3];\n\t"
+      "cp.async.bulk.commit_group;" ::"l"(map),
+      "r"(x), "r"(y), "r"(tc::smem_addr(src))
+      : "memory");
+}
+// All but the N last stores of this thread have read their source.
+template <int N> __device__ __forceinline__ void stores_read() {
+  asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void stores_done() { asm volatile("cp.async.bulk.wait_group 0;" ::: "memory"); }
+
+// Column sums of 32 values a lane: lane l gets that of v[l] over the warp.
+__device__ __forceinline__ float transposed_sum(float (&v)[32], int lane) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) {
+    const bool up = lane & o;
+#pragma unroll
+    for (int j = 0; j < o; ++j) {
+      const float keep = up ? v[j + o] : v[j], send = up ? v[j] : v[j + o];
+      v[j] = keep + __shfl_xor_sync(0xffffffffu, send, o);
+    }
+  }
+  return v[0];
+}
+
+template <int BN, int EPI>
+__device__ __forceinline__ bool io_epilogue(const Args &a, const CUtensorMap *to, const CUtensorMap *tx, uint8_t *bufs,
+                                            float *sbiases, uint64_t *xbars, uint64_t *tfull, uint64_t *tempty,
+                                            uint32_t tmem, int ew, int lane) {
+  using namespace tc;
+  constexpr uint32_t LIMIT = 1u << 26;
+  constexpr int BW = BN / 4, NCH = BW / 32, NB = io_bufs<EPI>();
+  constexpr bool EXTRA = EPI >= RES;
+  const Epi &e = a.g.e;
+  const int quarter = ew & 3, cols = (ew >> 2) * BW;
+  const uint32_t tq = tmem + ((uint32_t)(32 * quarter) << 16) + cols;
+  uint8_t *buf = bufs + ew * NB * IO_BUF;
+  float *sbias = sbiases + ew * 64;
+  uint64_t *xbar = xbars + ew * NB;
+  const int sw = (lane >> 1) & 3;   // swizzle of this lane's row
+  // lane 0's loads of the extra operand: next tile, chunk and buffer
+  int pi = blockIdx.x, pc = 0, pb = 0;
+  auto load_next = [&] {
+    for (; pi < a.s.tiles; pi += gridDim.x, pc = 0) {
+      const Tile t = tile_of(a.g, a.s, pi);
+      const int n = t.n0 + cols + 32 * pc, m = t.m0 + 32 * quarter;
+      if (pc < NCH && n < a.g.N && m < a.g.M) {
+        mbar_arrive_expect_tx(&xbar[pb], IO_BUF);
+        tma_load_2d(buf + pb * IO_BUF, tx, n, m, &xbar[pb]);
+        ++pc;
+        if (++pb == NB) pb = 0;
+        return;
+      }
+    }
+  };
+  if (EXTRA && lane == 0) {
+    load_next();
+    load_next();
+  }
+  int u = 0, b = 0, bias_of = -1;
+  uint32_t xph = 0;
+  float sum[NCH];
+#pragma unroll
+  for (int k = 0; k < NCH; ++k) sum[k] = 0.f;
+  bool ok = true;
+  for (int i = blockIdx.x; i < a.s.tiles && ok; i += gridDim.x) {
+    const Tile t = tile_of(a.g, a.s, i);
+    const int nw = t.n0 + cols, mw = t.m0 + 32 * quarter;
+    if (EPI != PLAIN && nw != bias_of) {   // a CTA's tiles mostly share their columns
+      bias_of = nw;
+      __syncwarp();
+#pragma unroll
+      for (int k = 0; k < NCH; ++k)
+        sbias[32 * k + lane] = e.bias && nw + 32 * k + lane < a.g.N ? __ldg(e.bias + nw + 32 * k + lane) : 0.f;
+      __syncwarp();
+    }
+    ok = __all_sync(0xffffffffu, mbar_wait(&tfull[u & 1], (u >> 1) & 1, LIMIT));
+    tc_fence_after();
+    int c = 0;
+#pragma unroll 1
+    for (; ok && c < NCH; ++c) {
+      const int n = nw + 32 * c;
+      if (n >= a.g.N || mw >= a.g.M) break;
+      float v[32];
+      tmem_ld_32x32b_x32(tq + (u & 1) * BN + 32 * c, v);
+      if (EPI != PLAIN) {
+        if (e.bias) {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) {
+            const float4 b4 = *reinterpret_cast<const float4 *>(sbias + 32 * c + 4 * j);
+            const f2 p = add2({v[4 * j], v[4 * j + 1]}, {b4.x, b4.y}), q = add2({v[4 * j + 2], v[4 * j + 3]}, {b4.z, b4.w});
+            v[4 * j] = p.x; v[4 * j + 1] = p.y; v[4 * j + 2] = q.x; v[4 * j + 3] = q.y;
+          }
+        }
+#define E2F_EACH2(F)                                  \
+  _Pragma("unroll") for (int j = 0; j < 32; j += 2) { \
+    const f2 p = F(f2{v[j], v[j + 1]});               \
+    v[j] = p.x;                                       \
+    v[j + 1] = p.y;                                   \
+  }
+        if (EPI != DZ) {
+          if (e.act == E2F_ACT_SILU) { E2F_EACH2(silu) }
+          else if (e.act == E2F_ACT_GELU) { E2F_EACH2(gelu) }
+        } else if (e.act == E2F_ACT_SILU) { E2F_EACH2(silu_grad) }
+        else { E2F_EACH2(gelu_grad) }
+#undef E2F_EACH2
+      }
+      uint4 *row = reinterpret_cast<uint4 *>(buf + b * IO_BUF + lane * 64);
+      if (EXTRA) {
+        ok = __all_sync(0xffffffffu, mbar_wait(&xbar[b], xph, LIMIT));
+        if (!ok) break;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          const uint4 w = row[j ^ sw];
+#pragma unroll
+          for (int k = 0; k < 4; ++k) {
+            const uint32_t x = u4w(w, k);
+            const f2 y = {__uint_as_float(x << 16), __uint_as_float(x & 0xffff0000u)};
+            const f2 z = {v[8 * j + 2 * k], v[8 * j + 2 * k + 1]}, r = EPI == RES ? add2(z, y) : mul2(z, y);
+            v[8 * j + 2 * k] = r.x;
+            v[8 * j + 2 * k + 1] = r.y;
+          }
+        }
+        // the buffer of the chunk before has left: the chunk after the next goes there
+        if (lane == 0) {
+          stores_read<0>();
+          load_next();
+        }
+      } else {
+        if (lane == 0) stores_read<1>();
+        __syncwarp();
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        row[j ^ sw] = make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
+                                 pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
+      fence_async_smem();
+      __syncwarp();
+      if (lane == 0) tma_store_2d(to, buf + b * IO_BUF, n, mw);
+      if (++b == NB) { b = 0; xph ^= 1; }
+      if (EPI == DZ && e.colpart) {
+        const float s = transposed_sum(v, lane);
+        if (a.s.keep) sum[0] += s;
+        else if (n + lane < a.g.N) e.colpart[(size_t)(mw >> 5) * a.g.N + n + lane] = s;
+        const float s0 = sum[0];   // (the sums turn by one chunk: see below)
+        if (NCH == 2) { sum[0] = sum[NCH - 1]; sum[NCH - 1] = s0; }
+      }
+    }
+    if (EPI == DZ && NCH == 2 && c == 1) {   // once around
+      const float s0 = sum[0];
+      sum[0] = sum[NCH - 1];
+      sum[NCH - 1] = s0;
+    }
+    tc_fence_before();
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&tempty[u & 1]);
+    ++u;
+  }
+  if (lane == 0) stores_done();
+  if (EPI == DZ && a.s.keep && e.colpart) {   // row (CTA among those of its columns, quarter)
+    const int n0 = tile_of(a.g, a.s, blockIdx.x).n0 + cols;
+    float *row = e.colpart + (size_t)((int)blockIdx.x / a.s.nt * 4 + quarter) * a.g.N;
+#pragma unroll
+    for (int k = 0; k < NCH; ++k)
+      if (n0 + 32 * k + lane < a.g.N) row[n0 + 32 * k + lane] = sum[k];
+  }
+  return ok;
+}
+
+template <bool AMN, bool BMN, int BN, bool LONGK, int EPI, int EW, bool IO>
 __global__ void __launch_bounds__(threads<EW>(), 1)
 gemm_tma_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tbm,
+                const __grid_constant__ CUtensorMap to, const __grid_constant__ CUtensorMap tx,
                 const __grid_constant__ Args a) {
   using namespace tc;
-  constexpr int RING = ring<EW>(), STAGING = staging<EW>(), SBIAS = sbias<EW>(), ABYTES = BM * BK * 2, BBYTES = BN * BK * 2;
+  constexpr int RING = IO ? io_ring<EPI>() : ring<EW>(), STAGING = IO ? 16 * io_bufs<EPI>() * IO_BUF : staging<EW>(),
+                SBIAS = IO ? IO_SBIAS : sbias<EW>();
+  constexpr int ABYTES = BM * BK * 2, BBYTES = BN * BK * 2;
   constexpr uint32_t LIMIT = 1u << 26;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
   float *staging = reinterpret_cast<float *>(smem + RING);
   uint64_t *full = reinterpret_cast<uint64_t *>(smem + RING + STAGING + SBIAS), *empty = full + MAX_ST,
-           *tfull = empty + MAX_ST, *tempty = tfull + 2, *bfull = tempty + 2;
+           *tfull = empty + MAX_ST, *tempty = tfull + 2, *bfull = tempty + 2, *xbar = full + 32;
   // (stage counts known to the compiler where B moves with A: the issuing thread
   // is on the critical path there)
   constexpr bool BRES = EW == 16;
@@ -99,6 +292,8 @@ gemm_tma_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ 
     for (int i = 0; i < ST; ++i) { mbar_init(&full[i], 1); mbar_init(&empty[i], 1); }
     for (int i = 0; i < 2; ++i) { mbar_init(&tfull[i], 1); mbar_init(&tempty[i], EW); }
     mbar_init(bfull, 1);
+    if (IO && EPI >= RES)
+      for (int i = 0; i < 16 * io_bufs<EPI>(); ++i) mbar_init(&xbar[i], 1);
     mbar_fence_init();
   }
   __syncthreads();
@@ -166,7 +361,11 @@ gemm_tma_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ 
       }
       if (!ok) atomicExch(a.err, E2F_ERR_TIMEOUT);
     }
-  } else if (warp >= 4) {
+  } else if (IO && warp >= 4) {
+    const bool ok = io_epilogue<BN, EPI>(a, &to, &tx, smem + RING, reinterpret_cast<float *>(smem + RING + STAGING), xbar,
+                                         tfull, tempty, tmem, warp - 4, lane);
+    if (!ok && lane == 0) atomicExch(a.err, E2F_ERR_TIMEOUT);
+  } else if (!IO && warp >= 4) {
     if (LONGK) asm volatile("setmaxnreg.inc.sync.aligned.u32 232;");
     constexpr int BW = BN * 4 / EW;                              // columns of this warp
     const int ew = warp - 4, quarter = warp & 3, cols = (ew >> 2) * BW;   // TMEM lanes 32 quarter + ..
@@ -315,53 +514,71 @@ static EncodeFn encode_fn() {
   return fn;
 }
 
-// [rows][cols] bf16, row stride ld elements; boxes of box_rows x 64 columns.
-static bool encode(CUtensorMap *m, const void *p, long long rows, long long cols, long long ld, int box_rows) {
+// [rows][cols] bf16, row stride ld elements; boxes of box_rows x box_cols (64:
+// 128-byte swizzle, 32: 64-byte).
+static bool encode(CUtensorMap *m, const void *p, long long rows, long long cols, long long ld, int box_rows,
+                   int box_cols = 64) {
   const EncodeFn fn = encode_fn();
   if (!fn) return false;
   const cuuint64_t dims[2] = {(cuuint64_t)cols, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)ld * 2};
-  const cuuint32_t box[2] = {64, (cuuint32_t)box_rows}, es[2] = {1, 1};
+  const cuuint32_t box[2] = {(cuuint32_t)box_cols, (cuuint32_t)box_rows}, es[2] = {1, 1};
   return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void *>(p), dims, strides, box, es,
-            CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+            CU_TENSOR_MAP_INTERLEAVE_NONE, box_cols == 64 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool AMN, bool BMN, int BN, bool LONGK, int EPI, int EW>
+template <bool AMN, bool BMN, int BN, bool LONGK, int EPI, int EW, bool IO>
 static e2f_status launch_epi(const CUtensorMap &ta, const CUtensorMap &tb, Args a, cudaStream_t s) {
   // B stays in shared memory for the launch where every CTA has one column tile
-  // and three stages of A fit beside it (100,002 x 128 -> 512: two thirds of the
-  // L2 reads; the time is the epilogue's and stays).
+  // and three stages of A fit beside it.
+  constexpr int RING = IO ? io_ring<EPI>() : ring<EW>();
   const long long bres = (long long)a.s.nkb * BN * BK * 2, abytes = BM * BK * 2;
-  a.bres = EW == 16 && a.s.fixed && a.g.kper == a.s.nkb && bres + 3 * abytes <= ring<EW>() ? (int)bres : 0;
-  a.st = std::min<int>(MAX_ST, (ring<EW>() - a.bres) / (a.bres ? (int)abytes : stage_bytes<BN>()));
-  constexpr auto k = gemm_tma_kernel<AMN, BMN, BN, LONGK, EPI, EW>;
-  E2F_CUDA_TRY(allow_smem<k>(smem_bytes<EW>(), LONGK ? 168 : 0));
-  E2F_LIN_LAUNCH(a.g, k, a.grid, threads<EW>(), smem_bytes<EW>(), s, ta, tb, a);
+  a.bres = EW == 16 && a.s.fixed && a.g.kper == a.s.nkb && bres + 3 * abytes <= RING ? (int)bres : 0;
+  a.st = std::min<int>(MAX_ST, (RING - a.bres) / (a.bres ? (int)abytes : stage_bytes<BN>()));
+  CUtensorMap to{}, tx{};
+  if (IO) {
+    const Epi &e = a.g.e;
+    if (!encode(&to, e.out, a.g.M, a.g.N, e.ldo, 32, 32) ||
+        (EPI >= RES && !encode(&tx, e.extra, a.g.M, a.g.N, e.lde, 32, 32))) {
+      set_cuda_error(cudaErrorInvalidValue, "cuTensorMapEncodeTiled");
+      return E2F_ERR_CUDA;
+    }
+  }
+  constexpr auto k = gemm_tma_kernel<AMN, BMN, BN, LONGK, EPI, EW, IO>;
+  constexpr size_t smem = IO ? io_smem<EPI>() : smem_bytes<EW>();
+  E2F_CUDA_TRY(allow_smem<k>(smem, LONGK ? 168 : 0));
+  E2F_LIN_LAUNCH(a.g, k, a.grid, threads<EW>(), smem, s, ta, tb, to, tx, a);
   return E2F_OK;
+}
+
+template <bool AMN, bool BMN, int BN, bool LONGK, int EPI>
+static e2f_status launch_kind(const CUtensorMap &ta, const CUtensorMap &tb, const Args &a, cudaStream_t s) {
+  if constexpr (!LONGK) {
+    const Epi &e = a.g.e;
+    if (a.g.kper <= short_k(EPI)) {
+      const bool io = e.mode != MODE_PART && e.out && e.otype == E2F_BF16 && tma_operand(e.out, e.ldo) &&
+                      (EPI < RES || (e.etype == E2F_BF16 && tma_operand(e.extra, e.lde)));
+      if (io) return launch_epi<AMN, BMN, BN, false, EPI, 16, true>(ta, tb, a, s);
+      return launch_epi<AMN, BMN, BN, false, EPI, 16, false>(ta, tb, a, s);
+    }
+  }
+  return launch_epi<AMN, BMN, BN, LONGK, EPI, 8, false>(ta, tb, a, s);
 }
 
 template <bool AMN, bool BMN, int BN, bool LONGK>
 static e2f_status launch(const CUtensorMap &ta, const CUtensorMap &tb, const Args &a, cudaStream_t s) {
-  const int kind = epi_kind(a.g.e);
-  constexpr int W = LONGK ? 8 : 16;
-  const bool wide = !LONGK && a.g.kper <= short_k(kind);
-#define E2F_LIN_EPI(E)                                                                \
-  return wide ? launch_epi<AMN, BMN, BN, LONGK, E, W>(ta, tb, a, s)              \
-              : launch_epi<AMN, BMN, BN, LONGK, E, 8>(ta, tb, a, s)
   if constexpr (!AMN && !BMN) {
-    if (kind == DZ) E2F_LIN_EPI(DZ);
-    if (kind == RES) E2F_LIN_EPI(RES);
-    if (kind == ACT) E2F_LIN_EPI(ACT);
+    switch (epi_kind(a.g.e)) {
+      case DZ: return launch_kind<AMN, BMN, BN, LONGK, DZ>(ta, tb, a, s);
+      case RES: return launch_kind<AMN, BMN, BN, LONGK, RES>(ta, tb, a, s);
+      case ACT: return launch_kind<AMN, BMN, BN, LONGK, ACT>(ta, tb, a, s);
+      default: break;
+    }
   }
-  E2F_LIN_EPI(PLAIN);
-#undef E2F_LIN_EPI
+  return launch_kind<AMN, BMN, BN, LONGK, PLAIN>(ta, tb, a, s);
 }
 
 }  // namespace tma
-
-bool tma_operand(const void *p, long long ld) {
-  return ((reinterpret_cast<uintptr_t>(p) | (uintptr_t)(ld * 2)) & 15) == 0;
-}
 
 // A bf16 product of aligned operands, split into `splits` parts of g.kper
 // contraction blocks (MODE_PART when there are several); bn = 128 or 256.

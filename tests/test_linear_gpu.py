@@ -320,3 +320,34 @@ def test_streams_and_graphs(cuda_ok):
             for _, o in graphs:
                 assert all(torch.equal(p, q) for p, q in zip(o, want))
     assert e2f.stream_status() == 0
+
+
+@pytest.mark.parametrize("dt,ot", TYPES)
+def test_extreme_preactivations(cuda_ok, dt, ot):
+    """Pre-activations from -3e4 to 3e4 and +-infinity side by side (pairs share
+    a reciprocal): every output as in 64 bits, NaN exactly where silu(-inf) and
+    the products of infinities with zero give it."""
+    import torch
+    from atomistic_mlip_b200 import e2f
+    dt, ot = getattr(torch, dt), getattr(torch, ot)
+    N = 264
+    for M in (3, 200):
+        vals = torch.tensor([0.0, 1.0, -1.0, 20.0, -20.0, 60.0, -60.0, 90.0, -90.0, 700.0, -700.0, 3e4, -3e4, 1e-30, -1e-30, 0.5])
+        x = vals.repeat(M, 1).to("cuda", dt)
+        sel = torch.arange(N) % 16
+        W = torch.zeros(N, 16)
+        W[torch.arange(N), sel] = 1.0
+        W = W.to("cuda", dt)
+        dy = torch.ones(M, N, device="cuda", dtype=ot)
+        for act in ("silu", "gelu"):
+            out = e2f.linear_forward(x, W, act=act, out_dtype=ot)
+            _check_forward(out, x, W, None, None, act)
+            _check_backward(*e2f.linear_backward(x, W, dy, act=act, need_bias=True), x, W, None, dy, act)
+            b = torch.zeros(N, device="cuda")
+            b[5], b[6], b[8] = float("inf"), float("-inf"), float("nan")
+            out = e2f.linear_forward(x, W, bias=b, act=act, out_dtype=ot)
+            keep = torch.ones(N, dtype=torch.bool, device="cuda")
+            keep[torch.tensor([5, 6, 8])] = False
+            _check_forward(out[:, keep], x, W[keep], None, None, act)
+            assert bool((out[:, 5] == float("inf")).all()) and bool(torch.isnan(out[:, 6]).all())
+            assert bool(torch.isnan(out[:, 8]).all())
