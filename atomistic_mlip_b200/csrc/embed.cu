@@ -140,6 +140,41 @@ __global__ void __launch_bounds__(NT) embed_fwd_kernel(const I *__restrict__ ids
   }
 }
 
+// Q = 1 and long rows: a warp per row, the id read once, eight vectors of a lane
+// in flight (16,381 rows of 770 bf16: the flat kernel looks the id up for every
+// vector, which costs it twice the time where a vector is two elements).
+template <typename I, typename T, typename O, int VE>
+__global__ void __launch_bounds__(NT) embed_row_kernel(const I *__restrict__ ids, long long N, int DV,
+                                                       const T *__restrict__ table, long long V, float scale,
+                                                       O *__restrict__ out, int *err) {
+  constexpr int U = 8;
+  const int lane = threadIdx.x & 31;
+  const long long row = (long long)blockIdx.x * (NT / 32) + (threadIdx.x >> 5);
+  if (row >= N) return;
+  const long long id = (long long)ids[row];
+  const bool live = id >= 0 && id < V;
+  if (!live && id != -1 && lane == 0) atomicExch(err, E2F_ERR_DOMAIN);
+  const T *src = table + (live ? (size_t)id * ((size_t)DV * VE) : 0);
+  O *dst = out + (size_t)row * ((size_t)DV * VE);
+  for (int c0 = lane; c0 < DV; c0 += 32 * U) {
+    float v[U][VE];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+      for (int k = 0; k < VE; ++k) v[u][k] = 0.f;
+      if (live && c0 + 32 * u < DV) Vec<T, VE>::load(src + (size_t)(c0 + 32 * u) * VE, v[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (c0 + 32 * u < DV) {
+        float w[VE];
+#pragma unroll
+        for (int k = 0; k < VE; ++k) w[k] = scale * v[u][k];
+        Vec<O, VE>::store(dst + (size_t)(c0 + 32 * u) * VE, w);
+      }
+  }
+}
+
 static bool aligned_to(const void *p, size_t b) { return (reinterpret_cast<uintptr_t>(p) & (b - 1)) == 0; }
 
 template <typename I, typename T, typename O, int VE>
@@ -149,6 +184,11 @@ static e2f_status launch_fwd(const I *ids, int64_t N, const T *table, int64_t V,
   if (!err) return E2F_ERR_CUDA;
   const int DV = D / VE, VR = (int)((long long)Q * DV);
   const long long nvec = (long long)N * VR;
+  if (Q == 1 && DV >= 64) {
+    E2F_LAUNCH((embed_row_kernel<I, T, O, VE>), (unsigned)((N + NT / 32 - 1) / (NT / 32)), NT, 0, s, ids, (long long)N, DV,
+               table, (long long)V, scale, out, err);
+    return E2F_OK;
+  }
   constexpr int per = fwd_u<VE, O>() * NT;
   const long long grid = (nvec + per - 1) / per;
   if (grid > INT32_MAX) return E2F_ERR_UNSUPPORTED;
@@ -157,14 +197,16 @@ static e2f_status launch_fwd(const I *ids, int64_t N, const T *table, int64_t V,
   return E2F_OK;
 }
 
-// Widest vector whose loads and stores are aligned: 16 bytes of the narrower
-// type, else two or one elements.
+// Widest vector whose loads and stores are aligned: 16 bytes of the wider type
+// where they differ, else four (bf16), two or one elements.
 template <typename I, typename T, typename O>
 static e2f_status pick_fwd(const I *ids, int64_t N, const T *table, int64_t V, int D, float scale, int Q, O *out,
                            cudaStream_t s) {
   constexpr int W = sizeof(T) == 2 && sizeof(O) == 2 ? 8 : 4;
   if (D % W == 0 && aligned_to(table, W * sizeof(T)) && aligned_to(out, W * sizeof(O)))
     return launch_fwd<I, T, O, W>(ids, N, table, V, D, scale, Q, out, s);
+  if (W == 8 && D % 4 == 0 && aligned_to(table, 4 * sizeof(T)) && aligned_to(out, 4 * sizeof(O)))
+    return launch_fwd<I, T, O, 4>(ids, N, table, V, D, scale, Q, out, s);
   if (D % 2 == 0 && aligned_to(table, 2 * sizeof(T)) && aligned_to(out, 2 * sizeof(O)))
     return launch_fwd<I, T, O, 2>(ids, N, table, V, D, scale, Q, out, s);
   return launch_fwd<I, T, O, 1>(ids, N, table, V, D, scale, Q, out, s);

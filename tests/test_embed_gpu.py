@@ -32,6 +32,7 @@ FWD = [  # N, V, D, Q, kind
     (0, 5, 8, 9, "uniform"), (1, 1, 1, 1, "one"), (24, 119, 8, 9, "species"), (7, 3, 3, 4, "padded"),
     (300, 1000, 130, 1, "uniform"), (33, 70000, 770, 1, "uniform"), (1025, 119, 128, 25, "padded"),
     (513, 17, 1, 1, "uniform"), (40, 9, 1023, 2, "uniform"), (9, 4, 64, 49, "all_padded"), (300, 6, 12, 1, "uniform"),
+    (130, 50, 516, 1, "padded"), (17, 50, 2056, 1, "uniform"), (1001, 3, 65, 1, "padded"),
 ]
 
 
