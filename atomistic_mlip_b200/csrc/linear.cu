@@ -31,16 +31,23 @@ template <typename T, bool AMN, bool BMN> e2f_status gemm_reg(const Gemm &g, int
 // linear_skinny.cu
 template <typename T> e2f_status gemm_skinny(const Gemm &g, cudaStream_t s, int *rows_out);
 
+// linear_small.cu
+bool small_fit(int M, int N, int K, int dtype);
+bool small_grads_fit(int M, int N, int K, int dtype);
+template <typename T> e2f_status gemm_small(const Gemm &g, cudaStream_t s);
+template <typename T>
+e2f_status small_grads(const e2f_linear &p, const void *dz, long long ldz, void *gx, long long ldgx, void *gW, long long ldgw,
+                       const void *cp, int ctype, long long cld, int crows, float *gb, bool after, cudaStream_t s);
+
 constexpr int BM = 128, BN = 128, BK = 64, NT = 256;
 
 // ---------------------------------------------------------------------------
 // Partial sums of a split contraction added in a fixed order, then the
 // epilogue (with no partial sums: the epilogue of zero accumulators, act'(.) dy
-// = dy).  A CTA takes FROWS rows of 32 columns; a warp takes whole rows (one
-// element a lane) while there are few splits, else the eight warps share the
-// splits of a row.
+// = dy).  A CTA takes FROWS rows of 32 columns, a warp one of them, while there
+// are few splits; else the eight warps share the splits of a row.
 // ---------------------------------------------------------------------------
-constexpr int FROWS = 32;
+constexpr int FROWS = 8;
 __global__ void __launch_bounds__(NT) finish_kernel(const float *__restrict__ part, int splits, int M, int N,
                                                     const __grid_constant__ Epi e) {
   __shared__ float red[NT / 32][33];
@@ -51,14 +58,12 @@ __global__ void __launch_bounds__(NT) finish_kernel(const float *__restrict__ pa
   const float bias = e.bias && n < N ? e.bias[n] : 0.f;
   float csum = 0.f;
   if (n < N) {
-#pragma unroll
-    for (int r = 0; r < FROWS / 8; ++r) {
-      const long long m = m0 + warp + 8 * r;
-      if (m >= M) break;
+    const long long m = m0 + warp;
+    if (m < M) {
       float v = 0.f;
 #pragma unroll 8
       for (int s = 0; s < splits; ++s) v += part[((size_t)s * M + m) * N + n];
-      csum += epi_elem(e, m, n, v, bias);
+      csum = epi_elem(e, m, n, v, bias);
     }
   }
   if (e.mode == MODE_DZ && e.colpart) {
@@ -129,9 +134,9 @@ static int sm_count() {   // one kind of device
   return n;
 }
 
-// Partial rows of column sums that a MODE_DZ product leaves at most: one of 32
-// rows, or four of a 128-row tile.
-static int64_t colpart_rows(int64_t M) { return 4 * ((M + BM - 1) / BM); }
+// Partial rows of column sums that a MODE_DZ product leaves at most: one of eight
+// rows (finish_kernel, streamed rows), of 32, or four of a 128-row tile.
+static int64_t colpart_rows(int64_t M) { return (M + 7) / 8 + 4; }
 
 template <typename T, bool AMN, bool BMN> struct Path {
   static bool tma(const Gemm &) { return false; }
@@ -149,6 +154,10 @@ template <typename T, bool AMN, bool BMN>
 static e2f_status run_gemm(Gemm g, cudaStream_t s, int *rows_out = nullptr) {
   if constexpr (!AMN && !BMN) {
     if (g.M <= 8 || g.N <= 8) return gemm_skinny<T>(g, s, rows_out);
+    if (small_fit(g.M, g.N, g.K, sizeof(T) == 4 ? E2F_F32 : E2F_BF16)) {
+      if (rows_out) *rows_out = (g.M + 31) / 32;
+      return gemm_small<T>(g, s);
+    }
   }
   const int mt = (g.M + BM - 1) / BM, nt = (g.N + BN - 1) / BN, nkb = (g.K + BK - 1) / BK;
   // Fewer tiles than SMs: the contraction is split so that every SM has a
@@ -179,7 +188,7 @@ static e2f_status run_gemm(Gemm g, cudaStream_t s, int *rows_out = nullptr) {
     g.part = ws.as<float>();
     g.e.mode = MODE_PART;
   }
-  if (rows_out) *rows_out = (int)((g.M + 31) / 32);
+  if (rows_out) *rows_out = (g.M + (splits > 1 ? FROWS : 32) - 1) / (splits > 1 ? FROWS : 32);
   e2f_status st = tma ? Path<T, AMN, BMN>::run_tma(g, splits, bn, sms, s, rows_out)
                       : gemm_reg<T, AMN, BMN>(g, splits, bn, sms, s);
   if (st != E2F_OK || splits == 1) return st;
@@ -255,6 +264,8 @@ static e2f_status backward(const e2f_linear &p, const void *dy, int64_t ldg, int
     if (prod) { dz = ws.p; ldz = lddz; }
     cp = g.e.colpart; ctype = E2F_F32; cld = N;
   }
+  if (small_grads_fit(M, N, K, TT))
+    return small_grads<T>(p, dz, ldz, gx, ldgx, gW, ldgw, cp, ctype, cld, crows, gb, after, s);
   if (gb) {
     float *to = reinterpret_cast<float *>(ws.as<char>() + zb) + (size_t)cr * N, *other = to + (size_t)cr2 * N;
     for (;;) {

@@ -142,8 +142,8 @@ template <typename T, int R> static e2f_status launch(Args a, cudaStream_t s, in
   a.lpr_log2 = 0;
   while (a.lpr_log2 < 5 && (1 << a.lpr_log2) < nv) ++a.lpr_log2;
   const int rows = a.outs ? g.M : g.N, group = NW * (32 >> a.lpr_log2);
-  // column sums: 32 rows of x at least to a CTA, as many partial rows as a tiled product leaves at most
-  a.iters = a.outs ? std::max(1, 32 / group) : 1;
+  // Many rows: several groups to a CTA, which stages the small operand once.
+  a.iters = (int)std::min<long long>(16, std::max<long long>(1, (long long)rows / (group * 1184LL)));
   const long long grid = ((long long)rows + group * a.iters - 1) / (group * a.iters);
   if (rows_out) *rows_out = a.outs ? (int)grid : 1;
   if (vec) E2F_LIN_LAUNCH(g, (skinny_kernel<T, R, W>), (unsigned)grid, NT, 0, s, a);

@@ -447,7 +447,7 @@ def embed_forward(ids, table, scale: float = 1.0, Q: int = 1, out_dtype=None, ou
     N, (V, D) = ids.shape[0], table.shape
     it, tt = _id_code(ids), _float_code(table, "table")
     if out is None:
-        out = table.new_empty((N, Q, D), dtype=out_dtype or torch.float32)
+        out = torch.empty(N, Q, D, dtype=out_dtype or torch.float32, device=table.device)
     elif out.shape != (N, Q, D) or not out.is_contiguous() or (out_dtype is not None and out.dtype != out_dtype):
         raise ValueError(f"out must be contiguous {(N, Q, D)}, of out_dtype if that is given")
     _call("e2f_embed_forward", stream, (ids, table, out), ids.data_ptr(), it, N, table.data_ptr(), tt, V, D, scale, Q,
@@ -471,7 +471,7 @@ def embed_backward(ids, grad_out, V: int, scale: float = 1.0, grad_table=None, a
     if grad_table is None:
         if accumulate:
             raise ValueError("accumulate needs grad_table")
-        grad_table = grad_out.new_empty((V, D), dtype=torch.float32)
+        grad_table = torch.empty(V, D, dtype=torch.float32, device=grad_out.device)
     elif grad_table.shape != (V, D) or not grad_table.is_contiguous() or grad_table.dtype != torch.float32:
         raise ValueError(f"grad_table must be contiguous float32 {(V, D)}")
     _call("e2f_embed_backward", stream, (ids, grad_out, grad_table), ids.data_ptr(), it, N, grad_out.data_ptr(), gt, V,
@@ -520,7 +520,7 @@ def linear_forward(x, W, bias=None, residual=None, act: str = "none", out=None, 
     (x's unless given by out_dtype or out) and may be out itself."""
     p, M, K, N = _linear_struct(x, W, bias, act)
     if out is None:
-        out = x.new_empty((M, N), dtype=out_dtype)
+        out = x.new_empty(M, N) if out_dtype is None else _torch().empty(M, N, dtype=out_dtype, device=x.device)
     elif out_dtype is not None and out.dtype != out_dtype:
         raise ValueError("out has another type than out_dtype")
     ldo, ldr = _ld(out, M, N, "out"), N
@@ -545,20 +545,20 @@ def linear_backward(x, W, grad_out, bias=None, act: str = "none", need_x: bool =
     ldg = _ld(grad_out, M, N, "grad_out")
     if need_bias is None:
         need_bias = bias is not None
-    gb = x.new_empty((N,), dtype=torch.float32) if need_bias else None
+    gb = torch.empty(N, dtype=torch.float32, device=x.device) if need_bias else None
     ldgx = ldgw = K
     if grad_x is not None:
         ldgx = _ld(grad_x, M, K, "grad_x")
         if grad_x.dtype != x.dtype:
             raise ValueError(f"grad_x has type {grad_x.dtype}, x {x.dtype}")
     elif need_x:
-        grad_x = x.new_empty((M, K))
+        grad_x = x.new_empty(M, K)
     if grad_W is not None:
         ldgw = _ld(grad_W, N, K, "grad_W")
         if grad_W.dtype != x.dtype:
             raise ValueError(f"grad_W has type {grad_W.dtype}, x {x.dtype}")
     elif need_W:
-        grad_W = x.new_empty((N, K))
+        grad_W = x.new_empty(N, K)
     _call("e2f_linear_backward", stream, (x, W, bias, grad_out, grad_x, grad_W), ctypes.byref(p), grad_out.data_ptr(),
           ldg, _float_code(grad_out, "grad_out"), _ptr(grad_x), ldgx, _ptr(grad_W), ldgw, _ptr(gb))
     return grad_x, grad_W, gb
