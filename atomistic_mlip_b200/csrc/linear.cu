@@ -153,7 +153,7 @@ template <bool AMN, bool BMN> struct Path<__nv_bfloat16, AMN, BMN> {
 template <typename T, bool AMN, bool BMN>
 static e2f_status run_gemm(Gemm g, cudaStream_t s, int *rows_out = nullptr) {
   if constexpr (!AMN && !BMN) {
-    if (g.M <= 8 || g.N <= 8) return gemm_skinny<T>(g, s, rows_out);
+    if (g.M <= 2 || g.N <= 2) return gemm_skinny<T>(g, s, rows_out);
     if (small_fit(g.M, g.N, g.K, sizeof(T) == 4 ? E2F_F32 : E2F_BF16)) {
       if (rows_out) *rows_out = (g.M + 31) / 32;
       return gemm_small<T>(g, s);

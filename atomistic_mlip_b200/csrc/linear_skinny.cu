@@ -1,12 +1,16 @@
-// Linear layers with at most eight rows (a serving step) or at most eight
-// outputs (the last layer of a readout): no tile to fill, the larger operand is
-// streamed once and bounds the time.
+// Linear layers with one or two rows (a serving step) or outputs (the last layer
+// of a readout): no tile to fill, the larger operand is streamed once and bounds
+// the time.  (From three on the tiled kernels win: at eight rows of 4,096 x 4,096
+// bf16 the reads of the small operand took 120 us here, 16 us there.)
 //
 // The streamed rows are W's (few x rows) or x's (few outputs).  LPR lanes share
-// one of them, 32 / LPR rows a warp; every lane holds R partial sums, one per
-// row of the small operand, which waits in shared memory as fp32, KC columns at
-// a time.  The sums are joined by shuffles in a fixed order.  fp32 and bf16
-// multiply in fp32 here.
+// RPT of them, RPT * 32 / LPR rows a warp; every lane holds RPT x R partial sums,
+// R rows of the small operand, which waits in shared memory as fp32, KC columns
+// at a time (eight consecutive ones in two halves, so that the lanes' 16-byte
+// reads do not meet in a bank).  Four rows a lane read each of its values once
+// for all four and keep four loads in flight where a row is short; one row a lane
+// where there would not be CTAs enough.  The sums are joined by shuffles in a
+// fixed order.  fp32 and bf16 multiply in fp32 here.
 #include <algorithm>
 
 #include "linear.cuh"
@@ -15,7 +19,7 @@ namespace e2f {
 namespace lin {
 namespace skinny {
 
-constexpr int NT = 256, NW = NT / 32, KC = 1024;
+constexpr int NT = 256, NW = NT / 32, KC = 4096;
 
 struct Args {
   Gemm g;
@@ -24,26 +28,36 @@ struct Args {
   int iters;       // row groups a CTA takes one after another
 };
 
-template <typename T, int VE> __device__ __forceinline__ void load_ve(const T *p, float (&v)[VE]) {
-  if constexpr (VE == 1) {
-    v[0] = to_f(*p);
-  } else if constexpr (sizeof(T) == 4) {
-    const float4 t = __ldg(reinterpret_cast<const float4 *>(p));
-    v[0] = t.x; v[1] = t.y; v[2] = t.z; v[3] = t.w;
-  } else {
-    const uint4 t = __ldg(reinterpret_cast<const uint4 *>(p));
+// VE consecutive elements of a streamed row as loaded, and as floats.
+template <typename T, int VE> struct Piece {
+  T v;
+  __device__ __forceinline__ void zero() { v = from_f<T>(0.f); }
+  __device__ __forceinline__ void load(const T *p) { v = *p; }
+  __device__ __forceinline__ void to(float (&f)[1]) const { f[0] = to_f(v); }
+};
+template <> struct Piece<float, 4> {
+  float4 v;
+  __device__ __forceinline__ void zero() { v = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ void load(const float *p) { v = __ldg(reinterpret_cast<const float4 *>(p)); }
+  __device__ __forceinline__ void to(float (&f)[4]) const { f[0] = v.x; f[1] = v.y; f[2] = v.z; f[3] = v.w; }
+};
+template <> struct Piece<__nv_bfloat16, 8> {
+  uint4 v;
+  __device__ __forceinline__ void zero() { v = make_uint4(0u, 0u, 0u, 0u); }
+  __device__ __forceinline__ void load(const __nv_bfloat16 *p) { v = __ldg(reinterpret_cast<const uint4 *>(p)); }
+  __device__ __forceinline__ void to(float (&f)[8]) const {
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-      v[2 * i] = __uint_as_float(u4w(t, i) << 16);
-      v[2 * i + 1] = __uint_as_float(u4w(t, i) & 0xffff0000u);
+      f[2 * i] = __uint_as_float(u4w(v, i) << 16);
+      f[2 * i + 1] = __uint_as_float(u4w(v, i) & 0xffff0000u);
     }
   }
-}
+};
 
 // VE: elements of a streamed row a load takes (16 bytes, or 1 at any alignment).
-template <typename T, int R, int VE>
+template <typename T, int R, int VE, int RPT>
 __global__ void __launch_bounds__(NT) skinny_kernel(const __grid_constant__ Args a) {
-  __shared__ float sm[R][KC];
+  __shared__ __align__(16) float sm[R][KC];
   __shared__ float red[NW][R];
   after_previous();
   const Gemm &g = a.g;
@@ -53,35 +67,37 @@ __global__ void __launch_bounds__(NT) skinny_kernel(const __grid_constant__ Args
   const long long lds = a.outs ? g.lda : g.ldb, ldp = a.outs ? g.ldb : g.lda;
   const int rows = a.outs ? g.M : g.N, r = a.outs ? g.N : g.M;
   const int nchunk = (g.K + KC - 1) / KC;
+  constexpr int U = (VE == 1 ? 8 : 4) / (RPT == 1 ? 1 : 2);   // loads of a row in flight
   float csum[R];
 #pragma unroll
   for (int j = 0; j < R; ++j) csum[j] = 0.f;
   for (int it = 0; it < a.iters; ++it) {
-    const long long row = ((long long)blockIdx.x * a.iters + it) * (NW * RW) + warp * RW + (lane >> a.lpr_log2);
-    const bool live = row < rows;
-    const T *srow = S + (live ? (size_t)(row * lds) : 0);
-    float acc[R];
+    const long long row0 = (((long long)blockIdx.x * a.iters + it) * (NW * RW) + warp * RW + (lane >> a.lpr_log2)) * RPT;
+    float acc[RPT][R];
 #pragma unroll
-    for (int j = 0; j < R; ++j) acc[j] = 0.f;
+    for (int q = 0; q < RPT; ++q)
+#pragma unroll
+      for (int j = 0; j < R; ++j) acc[q][j] = 0.f;
     for (int c = 0; c < nchunk; ++c) {
       const int k0 = c * KC, kn = min(KC, g.K - k0);
-      constexpr int U = VE == 1 ? 8 : 4;   // loads in flight
       const int step = LPR * VE;
-      float v[U][VE];
+      Piece<T, VE> v[RPT][U];
       auto fetch = [&](int k) {
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
+        for (int q = 0; q < RPT; ++q)
 #pragma unroll
-          for (int e = 0; e < VE; ++e) v[u][e] = 0.f;
-          if (live && k + u * step < kn) load_ve<T, VE>(srow + k0 + k + u * step, v[u]);
-        }
+          for (int u = 0; u < U; ++u) {
+            v[q][u].zero();
+            if (row0 + q < rows && k + u * step < kn) v[q][u].load(S + (size_t)((row0 + q) * lds) + k0 + k + u * step);
+          }
       };
       fetch(li * VE);   // under way while the small operand is staged
       if (nchunk > 1 || it == 0) {
         __syncthreads();
-        for (int i = t; i < R * KC; i += NT) {
-          const int j = i / KC, k = i - j * KC;
-          if (k < kn) sm[j][k] = j < r ? to_f(P[(size_t)(j * ldp) + k0 + k]) : 0.f;
+        for (int i = t; i < R * kn; i += NT) {
+          const int j = R == 1 || i < kn ? 0 : 1, k = i - j * kn;
+          if (k < kn) sm[j][VE == 8 ? (k >> 3) * 4 + (k & 3) + ((k >> 2) & 1) * (KC / 2) : k] =
+              j < r ? to_f(P[(size_t)(j * ldp) + k0 + k]) : 0.f;
         }
         __syncthreads();
       }
@@ -91,29 +107,43 @@ __global__ void __launch_bounds__(NT) skinny_kernel(const __grid_constant__ Args
         for (int u = 0; u < U; ++u) {
           const int ku = k + u * step;
           if (ku >= kn) break;
+          float f[RPT][VE];
 #pragma unroll
-          for (int j = 0; j < R; ++j)
+          for (int q = 0; q < RPT; ++q) v[q][u].to(f[q]);
 #pragma unroll
-            for (int e = 0; e < VE; ++e) acc[j] = fmaf(v[u][e], sm[j][ku + e], acc[j]);
+          for (int j = 0; j < R; ++j) {
+            float p[VE];
+#pragma unroll
+            for (int e = 0; e < VE; ++e) p[e] = VE == 8 ? sm[j][(ku >> 1) + (e & 3) + (e >> 2) * (KC / 2)] : sm[j][ku + e];
+#pragma unroll
+            for (int q = 0; q < RPT; ++q)
+#pragma unroll
+              for (int e = 0; e < VE; ++e) acc[q][j] = fmaf(f[q][e], p[e], acc[q][j]);
+          }
         }
       }
     }
-    for (int o = 1; o < LPR; o <<= 1)
 #pragma unroll
-      for (int j = 0; j < R; ++j) acc[j] += __shfl_xor_sync(0xffffffffu, acc[j], o);
-    float rsum = 0.f;
+    for (int q = 0; q < RPT; ++q) {
+      const long long row = row0 + q;
+      const bool live = row < rows;
+      for (int o = 1; o < LPR; o <<= 1)
 #pragma unroll
-    for (int j = 0; j < R; ++j) {
-      if (j < r && live && (j & (LPR - 1)) == li) {
-        const int n = a.outs ? j : (int)row;
-        const float d = epi_elem(g.e, a.outs ? row : j, n, acc[j], g.e.bias ? __ldg(g.e.bias + n) : 0.f);
-        csum[j] += d;
-        rsum += d;
+        for (int j = 0; j < R; ++j) acc[q][j] += __shfl_xor_sync(0xffffffffu, acc[q][j], o);
+      float rsum = 0.f;
+#pragma unroll
+      for (int j = 0; j < R; ++j) {
+        if (j < r && live && (j & (LPR - 1)) == li) {
+          const int n = a.outs ? j : (int)row;
+          const float d = epi_elem(g.e, a.outs ? row : j, n, acc[q][j], g.e.bias ? __ldg(g.e.bias + n) : 0.f);
+          csum[j] += d;
+          rsum += d;
+        }
       }
-    }
-    if (g.e.mode == MODE_DZ && g.e.colpart && !a.outs) {   // a column's rows are the lanes of one streamed row
-      for (int o = 1; o < LPR; o <<= 1) rsum += __shfl_xor_sync(0xffffffffu, rsum, o);
-      if (live && li == 0) g.e.colpart[row] = rsum;
+      if (g.e.mode == MODE_DZ && g.e.colpart && !a.outs) {   // a column's rows are the lanes of one streamed row
+        for (int o = 1; o < LPR; o <<= 1) rsum += __shfl_xor_sync(0xffffffffu, rsum, o);
+        if (live && li == 0) g.e.colpart[row] = rsum;
+      }
     }
   }
   if (g.e.mode == MODE_DZ && g.e.colpart && a.outs) {
@@ -132,6 +162,17 @@ __global__ void __launch_bounds__(NT) skinny_kernel(const __grid_constant__ Args
   }
 }
 
+template <typename T, int R, int VE, int RPT> static e2f_status launch_rpt(Args a, cudaStream_t s, int *rows_out) {
+  const Gemm &g = a.g;
+  const int rows = a.outs ? g.M : g.N, group = NW * (32 >> a.lpr_log2) * RPT;
+  // Many rows: several groups to a CTA, which stages the small operand once.
+  a.iters = (int)std::min<long long>(16, std::max<long long>(1, (long long)rows / (group * 1184LL)));
+  const long long grid = ((long long)rows + (long long)group * a.iters - 1) / ((long long)group * a.iters);
+  if (rows_out) *rows_out = a.outs ? (int)grid : 1;
+  E2F_LIN_LAUNCH(g, (skinny_kernel<T, R, VE, RPT>), (unsigned)grid, NT, 0, s, a);
+  return E2F_OK;
+}
+
 template <typename T, int R> static e2f_status launch(Args a, cudaStream_t s, int *rows_out) {
   const Gemm &g = a.g;
   constexpr int W = 16 / (int)sizeof(T);
@@ -141,28 +182,20 @@ template <typename T, int R> static e2f_status launch(Args a, cudaStream_t s, in
   const int nv = vec ? g.K / W : g.K;
   a.lpr_log2 = 0;
   while (a.lpr_log2 < 5 && (1 << a.lpr_log2) < nv) ++a.lpr_log2;
-  const int rows = a.outs ? g.M : g.N, group = NW * (32 >> a.lpr_log2);
-  // Many rows: several groups to a CTA, which stages the small operand once.
-  a.iters = (int)std::min<long long>(16, std::max<long long>(1, (long long)rows / (group * 1184LL)));
-  const long long grid = ((long long)rows + group * a.iters - 1) / (group * a.iters);
-  if (rows_out) *rows_out = a.outs ? (int)grid : 1;
-  if (vec) E2F_LIN_LAUNCH(g, (skinny_kernel<T, R, W>), (unsigned)grid, NT, 0, s, a);
-  else E2F_LIN_LAUNCH(g, (skinny_kernel<T, R, 1>), (unsigned)grid, NT, 0, s, a);
-  return E2F_OK;
+  const int rows = a.outs ? g.M : g.N;
+  const bool four = rows >= 148 * NW * (32 >> a.lpr_log2) * 4;   // a CTA on every SM all the same
+  if (vec) return four ? launch_rpt<T, R, W, 4>(a, s, rows_out) : launch_rpt<T, R, W, 1>(a, s, rows_out);
+  return four ? launch_rpt<T, R, 1, 4>(a, s, rows_out) : launch_rpt<T, R, 1, 1>(a, s, rows_out);
 }
 
 }  // namespace skinny
 
-// x W^T with M or N up to 8, both K-major.
+// x W^T with M or N up to 2, both K-major.
 template <typename T> e2f_status gemm_skinny(const Gemm &g, cudaStream_t s, int *rows_out) {
   skinny::Args a{};
   a.g = g;
-  a.outs = g.M > 8 || (g.N <= 8 && g.M > g.N);
-  const int r = a.outs ? g.N : g.M;
-  if (r == 1) return skinny::launch<T, 1>(a, s, rows_out);
-  if (r == 2) return skinny::launch<T, 2>(a, s, rows_out);
-  if (r <= 4) return skinny::launch<T, 4>(a, s, rows_out);
-  return skinny::launch<T, 8>(a, s, rows_out);
+  a.outs = g.M > 2 || (g.N <= 2 && g.M > g.N);
+  return (a.outs ? g.N : g.M) == 1 ? skinny::launch<T, 1>(a, s, rows_out) : skinny::launch<T, 2>(a, s, rows_out);
 }
 template e2f_status gemm_skinny<float>(const Gemm &, cudaStream_t, int *);
 template e2f_status gemm_skinny<__nv_bfloat16>(const Gemm &, cudaStream_t, int *);

@@ -56,6 +56,8 @@ SHAPES = [  # M, K, N, Q
     (3000, 128, 64, 25), (2051, 104, 205, 1), (700, 136, 520, 1), (257, 264, 1000, 9), (4099, 8, 24, 1),
     (33, 640, 1280, 1), (1, 4096, 9, 1), (40000, 24, 16, 1), (19000, 128, 512, 1), (16, 513, 129, 1),
     (2500, 2056, 1288, 1), (20001, 64, 264, 1), (5000, 1160, 640, 1), (128, 8, 8, 1),
+    (1, 5000, 130, 1), (2, 4104, 70, 1), (50003, 64, 2, 1), (50003, 7, 1, 9), (9000, 4200, 2, 1), (3, 1000, 999, 1), (8, 2048, 600, 1),
+    (2000, 72, 4, 1), (513, 40, 40, 1), (40, 513, 40, 1), (512, 30, 512, 25),
 ]
 TYPES = [("float32", "float32"), ("bfloat16", "bfloat16"), ("bfloat16", "float32"), ("float32", "bfloat16")]
 
