@@ -40,6 +40,7 @@ e2f_status small_grads(const e2f_linear &p, const void *dz, long long ldz, void 
                        const void *cp, int ctype, long long cld, int crows, float *gb, bool after, cudaStream_t s);
 
 constexpr int BM = 128, BN = 128, BK = 64, NT = 256;
+constexpr double ALIGN_WORK = 1 << 29;   // multiply-adds from which unaligned operands are copied first
 
 // ---------------------------------------------------------------------------
 // Partial sums of a split contraction added in a fixed order, then the
@@ -119,6 +120,27 @@ __global__ void __launch_bounds__(1024) colsum_kernel(const void *__restrict__ p
 #pragma unroll
     for (int j = 1; j < 32; ++j) s += red[j][lane];
     out[(size_t)blockIdx.y * N + n] = s;
+  }
+}
+
+// Rows of bf16 copied to a stride that is a multiple of 16 bytes: a row a warp,
+// lanes along it, eight loads in flight.
+__global__ void __launch_bounds__(NT) align_kernel(const __nv_bfloat16 *__restrict__ src, long long lds,
+                                                   __nv_bfloat16 *__restrict__ dst, long long ldd, long long rows, int cols) {
+  constexpr int U = 8;
+  const int lane = threadIdx.x & 31;
+  const long long r = (long long)blockIdx.x * (NT / 32) + (threadIdx.x >> 5);
+  if (r >= rows) return;
+  src += (size_t)(r * lds);
+  dst += (size_t)(r * ldd);
+  for (int c0 = lane; c0 < cols; c0 += 32 * U) {
+    __nv_bfloat16 v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (c0 + 32 * u < cols) v[u] = src[c0 + 32 * u];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+      if (c0 + 32 * u < cols) dst[c0 + 32 * u] = v[u];
   }
 }
 
@@ -202,10 +224,57 @@ static e2f_status run_gemm(Gemm g, cudaStream_t s, int *rows_out = nullptr) {
   return E2F_OK;
 }
 
+// bf16 x and W on 16-byte rows for large products, which then go by TMA: there the
+// copies cost less than element-wise loads in the product (100,001 x 127 -> 129
+// with its gradient 239 us, 170 us so; below 2^29 multiply-adds it is the other
+// way round).  fp32 operands pass through registers either way.  q: p with the
+// copies in place of what was unaligned; after: whether a kernel was launched.
 template <typename T>
-static e2f_status forward(const e2f_linear &p, const void *res, int64_t ldr, void *out, int64_t ldo, int out_dtype,
+static e2f_status align_operands(const e2f_linear &p, e2f_linear *q, Scratch *ws, bool *after, cudaStream_t s) {
+  *q = p;
+  if (sizeof(T) == 4) return E2F_OK;
+  if (p.M <= 2 || p.N <= 2 || (double)p.M * p.N * p.K < ALIGN_WORK) return E2F_OK;
+  auto aligned = [](const void *a, int64_t ld) {
+    return ((reinterpret_cast<uintptr_t>(a) | (uintptr_t)(ld * sizeof(T))) & 15) == 0;
+  };
+  const bool ax = !aligned(p.x, p.ldx), aw = !aligned(p.W, p.ldw);
+  if (!ax && !aw) return E2F_OK;
+  constexpr int per = 16 / (int)sizeof(T);
+  const int64_t ld = (p.K + per - 1) / per * per;
+  const size_t xb = ax ? (sizeof(T) * (size_t)p.M * ld + 255) & ~(size_t)255 : 0, wb = aw ? sizeof(T) * (size_t)p.N * ld : 0;
+  E2F_CUDA_TRY(ws->alloc(xb + wb, s));
+  auto copy = [&](const void *src, int64_t lds, char *dst, int64_t rows) {
+    const unsigned grid = (unsigned)((rows + NT / 32 - 1) / (NT / 32));
+    E2F_LAUNCH(align_kernel, grid, NT, 0, s, static_cast<const __nv_bfloat16 *>(src), (long long)lds,
+               reinterpret_cast<__nv_bfloat16 *>(dst), (long long)ld, (long long)rows, p.K);
+    return E2F_OK;
+  };
+  if (ax) {
+    const e2f_status st = copy(p.x, p.ldx, ws->as<char>(), p.M);
+    if (st != E2F_OK) return st;
+    q->x = ws->p;
+    q->ldx = ld;
+  }
+  if (aw) {
+    const e2f_status st = copy(p.W, p.ldw, ws->as<char>() + xb, p.N);
+    if (st != E2F_OK) return st;
+    q->W = ws->as<char>() + xb;
+    q->ldw = ld;
+  }
+  *after = true;
+  return E2F_OK;
+}
+
+template <typename T>
+static e2f_status forward(const e2f_linear &arg, const void *res, int64_t ldr, void *out, int64_t ldo, int out_dtype,
                           cudaStream_t s) {
+  Scratch copies;
+  e2f_linear p;
+  bool after = false;
+  const e2f_status st = align_operands<T>(arg, &p, &copies, &after, s);
+  if (st != E2F_OK) return st;
   Gemm g{};
+  g.after = after;
   g.A = p.x; g.lda = p.ldx; g.B = p.W; g.ldb = p.ldw;
   g.M = (int)p.M; g.N = p.N; g.K = p.K;
   g.e.mode = MODE_OUT; g.e.act = p.act; g.e.bias = p.bias;
@@ -215,10 +284,10 @@ static e2f_status forward(const e2f_linear &p, const void *res, int64_t ldr, voi
 }
 
 template <typename T>
-static e2f_status backward(const e2f_linear &p, const void *dy, int64_t ldg, int out_dtype, void *gx, int64_t ldgx,
+static e2f_status backward(const e2f_linear &arg, const void *dy, int64_t ldg, int out_dtype, void *gx, int64_t ldgx,
                            void *gW, int64_t ldgw, float *gb, cudaStream_t s) {
   constexpr int TT = sizeof(T) == 4 ? E2F_F32 : E2F_BF16;
-  const int M = (int)p.M, N = p.N, K = p.K;
+  const int M = (int)arg.M, N = arg.N, K = arg.K;
   if (M == 0) {   // empty sums
     if (gW) E2F_CUDA_TRY(cudaMemset2DAsync(gW, ldgw * sizeof(T), 0, K * sizeof(T), N, s));
     if (gb) E2F_CUDA_TRY(cudaMemsetAsync(gb, 0, sizeof(float) * N, s));
@@ -226,6 +295,13 @@ static e2f_status backward(const e2f_linear &p, const void *dy, int64_t ldg, int
   }
   const bool prod = gx || gW;
   if (!prod && !gb) return E2F_OK;
+  Scratch copies;
+  e2f_linear p;
+  bool after = false;
+  {
+    const e2f_status st = align_operands<T>(arg, &p, &copies, &after, s);
+    if (st != E2F_OK) return st;
+  }
   // dz: dy itself where there is no activation and the types agree
   const bool own = p.act != E2F_ACT_NONE || out_dtype != TT;
   const long long lddz = (N + 7) & ~7;
@@ -238,13 +314,13 @@ static e2f_status backward(const e2f_linear &p, const void *dy, int64_t ldg, int
   if (zb + cb) E2F_CUDA_TRY(ws.alloc(zb + cb, s));
   const void *dz = dy;
   long long ldz = ldg;
-  bool after = false;
   // what the column sums are taken of
   const void *cp = dy;
   int ctype = out_dtype, crows = M;
   long long cld = ldg;
   if (own) {
     Gemm g{};
+    g.after = after;
     g.A = p.x; g.lda = p.ldx; g.B = p.W; g.ldb = p.ldw;
     g.M = M; g.N = N; g.K = K;
     g.e.mode = MODE_DZ; g.e.act = p.act; g.e.bias = p.bias;
@@ -257,8 +333,8 @@ static e2f_status backward(const e2f_linear &p, const void *dy, int64_t ldg, int
       if (st != E2F_OK) return st;
     } else {
       g.e.bias = nullptr;
-      E2F_LAUNCH(finish_kernel, dim3((unsigned)((M + FROWS - 1) / FROWS), (unsigned)((N + 31) / 32)), NT, 0, s,
-                 (const float *)nullptr, 0, M, N, g.e);
+      const dim3 grid((unsigned)((M + FROWS - 1) / FROWS), (unsigned)((N + 31) / 32));
+      E2F_LIN_LAUNCH(g, finish_kernel, grid, NT, 0, s, (const float *)nullptr, 0, M, N, g.e);
     }
     after = true;
     if (prod) { dz = ws.p; ldz = lddz; }

@@ -180,8 +180,10 @@ template <typename T, int R> static e2f_status launch(Args a, cudaStream_t s, in
   const long long lds = a.outs ? g.lda : g.ldb;
   const bool vec = g.K % W == 0 && ((reinterpret_cast<uintptr_t>(S) | (uintptr_t)(lds * sizeof(T))) & 15) == 0;
   const int nv = vec ? g.K / W : g.K;
+  // two to four loads of a row to a lane: fewer shuffles and epilogues a warp than
+  // with one
   a.lpr_log2 = 0;
-  while (a.lpr_log2 < 5 && (1 << a.lpr_log2) < nv) ++a.lpr_log2;
+  while (a.lpr_log2 < 5 && (4 << a.lpr_log2) < nv) ++a.lpr_log2;
   const int rows = a.outs ? g.M : g.N;
   const bool four = rows >= 148 * NW * (32 >> a.lpr_log2) * 4;   // a CTA on every SM all the same
   if (vec) return four ? launch_rpt<T, R, W, 4>(a, s, rows_out) : launch_rpt<T, R, W, 1>(a, s, rows_out);
