@@ -44,8 +44,18 @@ __device__ __forceinline__ Tile tile_of(const Gemm &g, const Sched &a, int i) {
   return t;
 }
 
-struct Extra {   // 4 x 8 elements of residual or dL/dout: bf16 in lo, fp32 in lo and hi
+// A chunk's residual or dL/dout: 4 x 8 elements, bf16 in lo, fp32 in lo and hi;
+// where rows are not aligned, column n + lane of the 32 rows, a word each.
+struct Extra {
   uint4 lo[4], hi[4];
+  __device__ __forceinline__ uint32_t word(int r) const { return r < 16 ? u4w(lo[r >> 2], r & 3) : u4w(hi[(r - 16) >> 2], r & 3); }
+  __device__ __forceinline__ void word(int r, uint32_t v) {
+    uint4 &q = r < 16 ? lo[r >> 2] : hi[(r - 16) >> 2];
+    if ((r & 3) == 0) q.x = v;
+    else if ((r & 3) == 1) q.y = v;
+    else if ((r & 3) == 2) q.z = v;
+    else q.w = v;
+  }
 };
 
 // Eight elements of type T (float, __nv_bfloat16) as four pairs, from the raw words.
@@ -100,10 +110,26 @@ __device__ __forceinline__ Rows rows_of(const Gemm &g, int split, int m0, int la
   return r;
 }
 
-// The chunk's residual or dL/dout from column n on.
+// The chunk's residual or dL/dout from column n on; UA: rows of any alignment too.
+template <bool UA>
 __device__ __forceinline__ void load_extra(Extra &d, const Gemm &g, int vec, const Rows &rw, int n, int lane) {
   const int ng = n + (lane & 3) * 8, r8 = lane >> 2;
-  if (!vec || ng >= g.N) return;
+  if (!vec) {
+    if (!UA || n + lane >= g.N) return;
+    if (g.e.etype == E2F_F32) {
+      const uint32_t *p = static_cast<const uint32_t *>(g.e.extra) + (size_t)(rw.m0 * g.e.lde) + n + lane;
+#pragma unroll
+      for (int r = 0; r < 32; ++r, p += g.e.lde)
+        if (r < rw.n) d.word(r, __ldg(p));
+    } else {
+      const unsigned short *p = static_cast<const unsigned short *>(g.e.extra) + (size_t)(rw.m0 * g.e.lde) + n + lane;
+#pragma unroll
+      for (int r = 0; r < 32; ++r, p += g.e.lde)
+        if (r < rw.n) d.word(r, (uint32_t)__ldg(p) << 16);
+    }
+    return;
+  }
+  if (ng >= g.N) return;
   if (g.e.etype == E2F_F32) {
     const char *p = rw.extra + 4 * (size_t)ng;
 #pragma unroll
@@ -163,7 +189,11 @@ __device__ __forceinline__ void put_rows(const Rows &rw, const Extra &x, const f
 // x: the chunk's extra (load_extra); st: 4 KB, sbias: 32 floats of the warp.
 // DZ: the lane's column sums are added to cs where that is kept across tiles
 // (keep), else go to their row of e.colpart.
-template <int EPI, int PW, class Get>
+// UA: an unaligned chunk's extra was loaded with it and its 32 rows are unrolled.
+// Only the fp32 kernel does: 80,736 x 79 -> 429 172 -> 137 us there, while the
+// registers that it takes cost the others more (bf16 75 -> 86 us; aligned fp32
+// residuals of 8,192 x 1,024 -> 4,096 83 -> 90 us).
+template <int EPI, int PW, bool UA, class Get>
 __device__ __forceinline__ void epi_chunk(const Gemm &g, int vec, int split, const Rows &rw, int n, float bias,
                                           const Extra &x, f2 (&cs)[4], bool keep, float *st, float *sbias, int lane,
                                           Get get) {
@@ -260,29 +290,49 @@ __device__ __forceinline__ void epi_chunk(const Gemm &g, int vec, int split, con
     if (EPI == DZ && !keep && e.colpart) flush_colsum(cs, e.colpart + (size_t)(rw.m0 >> 5) * g.N, ng, g.N, lane);
   } else if (n + lane < g.N) {   // any alignment: lane = column
     const int nl = n + lane;
-    float *part = EPI != PLAIN || e.mode != MODE_PART ? nullptr : g.part + (size_t)split * g.M * g.N;
     float sum = 0.f;
-    for (int r0 = 0; r0 < 32 && r0 < rw.n; r0 += 8) {
-      float y[8];
-      if (EXTRA) {
+    if constexpr (UA) {
+      const bool of = e.mode == MODE_PART || e.otype == E2F_F32, store = EPI != DZ || e.out;
+      char *o = rw.out - (size_t)((long long)r8 * (rw.ostep / 8)) + (of ? 4 : 2) * (size_t)nl;   // row m0
 #pragma unroll
-        for (int r = 0; r < 8; ++r)
-          y[r] = r0 + r < rw.n ? load_as(e.extra, e.etype, (size_t)((rw.m0 + r0 + r) * e.lde) + nl) : 0.f;
+      for (int r = 0; r < 32; ++r, o += rw.ostep / 8) {
+        if (r < rw.n) {
+          float w = st[r * 32 + ((((lane >> 2) ^ (r & 7)) << 2) | (lane & 3))];
+          if (EXTRA) {
+            const float y = __uint_as_float(x.word(r));
+            w = EPI == RES ? w + y : w * y;
+            sum += w;
+          }
+          if (store) {
+            if (of) *reinterpret_cast<float *>(o) = w;
+            else *reinterpret_cast<__nv_bfloat16 *>(o) = __float2bfloat16_rn(w);
+          }
+        }
       }
-#pragma unroll
-      for (int r = 0; r < 8; ++r) {
-        const int row = r0 + r, m = rw.m0 + row;
-        if (row >= rw.n) break;
-        float w = st[row * 32 + ((((lane >> 2) ^ (row & 7)) << 2) | (lane & 3))];
-        if (part) {
-          part[(size_t)m * g.N + nl] = w;
-          continue;
-        }
+    } else {
+      float *part = EPI != PLAIN || e.mode != MODE_PART ? nullptr : g.part + (size_t)split * g.M * g.N;
+      for (int r0 = 0; r0 < 32 && r0 < rw.n; r0 += 8) {
+        float y[8];
         if (EXTRA) {
-          w = EPI == RES ? w + y[r] : w * y[r];
-          sum += w;
+#pragma unroll
+          for (int r = 0; r < 8; ++r)
+            y[r] = r0 + r < rw.n ? load_as(e.extra, e.etype, (size_t)((rw.m0 + r0 + r) * e.lde) + nl) : 0.f;
         }
-        if (EPI != DZ || e.out) store_as(e.out, e.otype, (size_t)(m * e.ldo) + nl, w);
+#pragma unroll
+        for (int r = 0; r < 8; ++r) {
+          const int row = r0 + r, m = rw.m0 + row;
+          if (row >= rw.n) break;
+          float w = st[row * 32 + ((((lane >> 2) ^ (row & 7)) << 2) | (lane & 3))];
+          if (part) {
+            part[(size_t)m * g.N + nl] = w;
+            continue;
+          }
+          if (EXTRA) {
+            w = EPI == RES ? w + y[r] : w * y[r];
+            sum += w;
+          }
+          if (EPI != DZ || e.out) store_as(e.out, e.otype, (size_t)(m * e.ldo) + nl, w);
+        }
       }
     }
     if (EPI == DZ && e.colpart) e.colpart[(size_t)(rw.m0 >> 5) * g.N + nl] = sum;

@@ -304,8 +304,9 @@ __global__ void __launch_bounds__(NT, 1) gemm_reg_kernel(const __grid_constant__
         if (cc >= a.s.bn || n >= g.N || mw >= g.M) break;
         Extra x;
         f2 cs[4];
-        if (EXTRA) load_extra(x, g, a.s.vec, rw, n, lane);
-        epi_chunk<EPI, 16>(g, a.s.vec, t.split, rw, n, c ? bias[1] : bias[0], x, cs, false, st, sbias, lane,
+        constexpr bool UA = sizeof(T) == 4 && !LONGK;
+        if (EXTRA) load_extra<UA>(x, g, a.s.vec, rw, n, lane);
+        epi_chunk<EPI, 16, UA>(g, a.s.vec, t.split, rw, n, c ? bias[1] : bias[0], x, cs, false, st, sbias, lane,
                            [&](int h, float (&v)[16]) {
           if constexpr (LONGK) {
 #pragma unroll

@@ -396,7 +396,7 @@ gemm_tma_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ 
       }
       constexpr bool EXTRA = EPI >= RES, AHEAD = EXTRA && !LONGK && EW == 8;   // registers for the next chunk's extra
       Extra x;
-      if (AHEAD && nw < a.g.N && mw < a.g.M) load_extra(x, a.g, a.s.vec, rw, nw, lane);
+      if (AHEAD && nw < a.g.N && mw < a.g.M) load_extra<false>(x, a.g, a.s.vec, rw, nw, lane);
       float acc[LONGK ? BW : 1];
       if (LONGK) {
 #pragma unroll
@@ -450,12 +450,12 @@ gemm_tma_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ 
         const bool more = c + 1 < NCH && n + 32 < a.g.N;
         Extra nx;
         if (EXTRA) {   // what the epilogue reads, on its way while the accumulators move
-          if (!AHEAD) load_extra(x, a.g, a.s.vec, rw, n, lane);
-          else if (more) load_extra(nx, a.g, a.s.vec, rw, n + 32, lane);
+          if (!AHEAD) load_extra<false>(x, a.g, a.s.vec, rw, n, lane);
+          else if (more) load_extra<false>(nx, a.g, a.s.vec, rw, n + 32, lane);
         }
         // (16 columns at a time where the extra's registers live beside them)
         constexpr int PW = EXTRA && EW == 16 ? 16 : 32;
-        epi_chunk<EPI, PW>(a.g, a.s.vec, t.split, rw, n, bias[0], x, sums[0], a.s.keep, st, sbias, lane,
+        epi_chunk<EPI, PW, false>(a.g, a.s.vec, t.split, rw, n, bias[0], x, sums[0], a.s.keep, st, sbias, lane,
                            [&](int h, float (&v)[PW]) {
           if constexpr (LONGK) {
 #pragma unroll
