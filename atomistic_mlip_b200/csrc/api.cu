@@ -156,7 +156,7 @@ static bool aligned_elem(const void *p, int32_t type) {
 static e2f_status validate_embed(int32_t id_type, int64_t N, int32_t dtype, int64_t V, int32_t D, float scale, int32_t Q) {
   if (id_type != E2F_I32 && id_type != E2F_I64) return E2F_ERR_UNSUPPORTED;
   if (!float_type(dtype)) return E2F_ERR_UNSUPPORTED;
-  if (N < 0 || N > INT32_MAX || V < 1 || V >= INT32_MAX || D < 1 || Q < 1) return E2F_ERR_INVALID_ARG;
+  if (N < 0 || N > E2F_MAX_ROWS || V < 1 || V > E2F_MAX_ROWS || D < 1 || Q < 1) return E2F_ERR_INVALID_ARG;
   if (D > (1 << 20) || (int64_t)Q * D > (1 << 30)) return E2F_ERR_UNSUPPORTED;
   if (!(scale > -INFINITY && scale < INFINITY)) return E2F_ERR_INVALID_ARG;
   return E2F_OK;
@@ -169,7 +169,7 @@ static e2f_status validate_linear(const e2f_linear *p, int32_t out_dtype) {
   if (!p) return E2F_ERR_INVALID_ARG;
   if (!float_type(p->dtype) || !float_type(out_dtype)) return E2F_ERR_UNSUPPORTED;
   if (p->act != E2F_ACT_NONE && p->act != E2F_ACT_SILU && p->act != E2F_ACT_GELU) return E2F_ERR_UNSUPPORTED;
-  if (p->M < 0 || p->M > INT32_MAX || p->K < 1 || p->N < 1) return E2F_ERR_INVALID_ARG;
+  if (p->M < 0 || p->M > E2F_MAX_ROWS || p->K < 1 || p->N < 1) return E2F_ERR_INVALID_ARG;
   if (p->K > (1 << 20) || p->N > (1 << 20)) return E2F_ERR_UNSUPPORTED;
   if (!stride_ok(p->ldx, p->K) || !stride_ok(p->ldw, p->K)) return E2F_ERR_INVALID_ARG;
   if (p->M > 0 && (!p->x || !p->W)) return E2F_ERR_INVALID_ARG;
@@ -350,7 +350,7 @@ e2f_status e2f_embed_forward(const void *ids, int32_t id_type, int64_t N, const 
   if (st != E2F_OK) return st;
   if (!float_type(out_dtype)) return E2F_ERR_UNSUPPORTED;
   if (N == 0) return E2F_OK;
-  if (!ids || !table || !out) return E2F_ERR_INVALID_ARG;
+  if (!ids || !table || !out || out == table || out == ids) return E2F_ERR_INVALID_ARG;
   if (!aligned_elem(ids, id_type) || !aligned_elem(table, dtype) || !aligned_elem(out, out_dtype))
     return E2F_ERR_INVALID_ARG;
   return embed_forward_impl(ids, id_type, N, table, dtype, V, D, scale, Q, out, out_dtype,
@@ -363,7 +363,7 @@ e2f_status e2f_embed_backward(const void *ids, int32_t id_type, int64_t N, const
   if (st != E2F_OK) return st;
   if (accumulate != 0 && accumulate != 1) return E2F_ERR_INVALID_ARG;
   if (!grad_table || !aligned_elem(grad_table, E2F_F32)) return E2F_ERR_INVALID_ARG;
-  if (N > 0 && (!ids || !grad_out)) return E2F_ERR_INVALID_ARG;
+  if (N > 0 && (!ids || !grad_out || grad_table == grad_out || grad_table == ids)) return E2F_ERR_INVALID_ARG;
   if (!aligned_elem(ids, id_type) || !aligned_elem(grad_out, dtype)) return E2F_ERR_INVALID_ARG;
   return embed_backward_impl(ids, id_type, N, grad_out, dtype, V, D, scale, Q, grad_table, accumulate,
                              static_cast<cudaStream_t>(stream));
@@ -375,7 +375,7 @@ e2f_status e2f_linear_forward(const e2f_linear *p, const void *residual, int64_t
   if (st != E2F_OK) return st;
   if (!stride_ok(ldo, p->N) || (residual && !stride_ok(ldr, p->N))) return E2F_ERR_INVALID_ARG;
   if (p->M == 0) return E2F_OK;
-  if (!out || out == p->x || out == p->W) return E2F_ERR_INVALID_ARG;
+  if (!out || out == p->x || out == p->W || out == p->bias) return E2F_ERR_INVALID_ARG;
   if (residual == out && ldr != ldo) return E2F_ERR_INVALID_ARG;
   if (!aligned_elem(out, out_dtype) || !aligned_elem(residual, out_dtype)) return E2F_ERR_INVALID_ARG;
   return linear_forward_impl(p, residual, ldr, out, ldo, out_dtype, static_cast<cudaStream_t>(stream));
@@ -390,6 +390,7 @@ e2f_status e2f_linear_backward(const e2f_linear *p, const void *grad_out, int64_
   if (p->M > 0 && !grad_out) return E2F_ERR_INVALID_ARG;
   for (const void *o : {(const void *)grad_x, (const void *)grad_W, (const void *)grad_bias})
     if (o && (o == p->x || o == p->W || o == p->bias || o == grad_out)) return E2F_ERR_INVALID_ARG;
+  if ((grad_x && (grad_x == grad_W || grad_x == grad_bias)) || (grad_W && grad_W == grad_bias)) return E2F_ERR_INVALID_ARG;
   if (!aligned_elem(grad_out, out_dtype) || !aligned_elem(grad_x, p->dtype) || !aligned_elem(grad_W, p->dtype) ||
       !aligned_elem(grad_bias, E2F_F32))
     return E2F_ERR_INVALID_ARG;

@@ -5,8 +5,10 @@
 //   backward   z  = x W^T + b (formed again: nothing but y leaves the forward),
 //              dz = dy act'(z),  dx = dz W,  dW = dz^T x,  db = sum_m dz
 //
-// All products run on the tensor cores.  bf16 operands are used as they are,
-// fp32 accumulation.  fp32 operands are split into three bf16 terms each,
+// Products run on the tensor cores (linear_tma.cu, linear_reg.cu), but for those
+// with one or two rows or outputs (linear_skinny.cu) and those too small to fill
+// them (linear_small.cu).  bf16 operands are used as they are, fp32
+// accumulation.  fp32 operands are split into three bf16 terms each,
 // x = h + m + l (8 + 8 + 8 significant bits: exact), and the products
 // h h', (h m' + m h' + h l' + l h' + m m') are summed in two accumulators; the
 // terms left out are below 2^-24 of a product, so the result is that of an
@@ -108,8 +110,8 @@ __global__ void __launch_bounds__(1024) colsum_kernel(const void *__restrict__ p
                                                       float *__restrict__ out) {
   __shared__ float red[32][33];
   after_previous();
-  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, n = blockIdx.x * 32 + lane;
-  const int p0 = blockIdx.y * CROWS, p1 = min(p0 + CROWS, P);
+  const int lane = threadIdx.x & 31, w = threadIdx.x >> 5, n = blockIdx.y * 32 + lane;
+  const int p0 = blockIdx.x * CROWS, p1 = min(p0 + CROWS, P);
   float s = 0.f;
   if (n < N)
 #pragma unroll 8
@@ -119,7 +121,7 @@ __global__ void __launch_bounds__(1024) colsum_kernel(const void *__restrict__ p
   if (w == 0 && n < N) {
 #pragma unroll
     for (int j = 1; j < 32; ++j) s += red[j][lane];
-    out[(size_t)blockIdx.y * N + n] = s;
+    out[(size_t)blockIdx.x * N + n] = s;
   }
 }
 
@@ -346,7 +348,7 @@ static e2f_status backward(const e2f_linear &arg, const void *dy, int64_t ldg, i
     float *to = reinterpret_cast<float *>(ws.as<char>() + zb) + (size_t)cr * N, *other = to + (size_t)cr2 * N;
     for (;;) {
       const int q = (crows + CROWS - 1) / CROWS;
-      const dim3 grid((unsigned)((N + 31) / 32), (unsigned)q);
+      const dim3 grid((unsigned)q, (unsigned)((N + 31) / 32));
       if (after) E2F_LAUNCH_AFTER(colsum_kernel, grid, 1024, 0, s, cp, ctype, cld, crows, N, q == 1 ? gb : to);
       else E2F_LAUNCH(colsum_kernel, grid, 1024, 0, s, cp, ctype, cld, crows, N, q == 1 ? gb : to);
       after = true;

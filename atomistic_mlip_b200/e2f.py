@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import ctypes
 import dataclasses
+import functools
 import os
 from typing import List, Optional, Sequence
 
@@ -433,7 +434,21 @@ def _call(fn: str, stream, tensors, *args):
         _check(code, fn)
 
 
-def embed_forward(ids, table, scale: float = 1.0, Q: int = 1, out_dtype=None, out=None, stream=None):
+def _on_stream(f):
+    """f(..., stream=s) with s as the current stream, so that what f allocates
+    comes from that stream's memory: neither work still pending elsewhere nor a
+    later allocation elsewhere can meet the kernels of the call."""
+    @functools.wraps(f)
+    def call(*args, stream=None, **kw):
+        if stream is None:
+            return f(*args, **kw)
+        with _torch().cuda.stream(stream):
+            return f(*args, stream=stream, **kw)
+    return call
+
+
+@_on_stream
+def embed_forward(ids, table, scale: float = 1.0, Q: int = 1, out_dtype=None, out=None, *, stream=None):
     """Features [N, Q, D] whose l = 0 row is scale * table[ids] and whose other
     rows are zero (Q = 1: an embedding lookup).  ids int32 or int64 [N], -1 for
     a padded row; table float32 or bfloat16 [V, D]; out_dtype float32 unless
@@ -455,7 +470,8 @@ def embed_forward(ids, table, scale: float = 1.0, Q: int = 1, out_dtype=None, ou
     return out
 
 
-def embed_backward(ids, grad_out, V: int, scale: float = 1.0, grad_table=None, accumulate: bool = False, stream=None):
+@_on_stream
+def embed_backward(ids, grad_out, V: int, scale: float = 1.0, grad_table=None, accumulate: bool = False, *, stream=None):
     """Gradient float32 [V, D] of embed_forward's table: scale * the sum of the
     l = 0 rows of grad_out (float32 or bfloat16 [N, Q, D] or [N, D]) over the
     rows of each id.  With accumulate the sums are added to grad_table.  Sums
@@ -513,7 +529,8 @@ def _linear_struct(x, W, bias, act: str):
     return Linear(code, ACT[act], M, K, N, x.data_ptr(), _ld(x, M, K, "x"), W.data_ptr(), _ld(W, N, K, "W"), bp), M, K, N
 
 
-def linear_forward(x, W, bias=None, residual=None, act: str = "none", out=None, out_dtype=None, stream=None):
+@_on_stream
+def linear_forward(x, W, bias=None, residual=None, act: str = "none", out=None, out_dtype=None, *, stream=None):
     """act(x W^T + bias) + residual [M, N].  x [M, K] and W [N, K] float32 or
     bfloat16 with any row stride (x may be features[:, 0] of [M, Q, K]), bias
     float32 [N], act "none", "silu" or "gelu"; residual has the output's type
@@ -533,8 +550,9 @@ def linear_forward(x, W, bias=None, residual=None, act: str = "none", out=None, 
     return out
 
 
+@_on_stream
 def linear_backward(x, W, grad_out, bias=None, act: str = "none", need_x: bool = True, need_W: bool = True,
-                    need_bias: Optional[bool] = None, grad_x=None, grad_W=None, stream=None):
+                    need_bias: Optional[bool] = None, grad_x=None, grad_W=None, *, stream=None):
     """(grad_x, grad_W, grad_bias) of sum(grad_out * linear_forward(x, W, bias,
     act=act)): the first two in x's type, grad_bias float32; None where not
     needed (grad_bias: needed if there is a bias, unless told).  grad_x and
@@ -573,32 +591,35 @@ class DeviceReadout:
         self.W1, self.b1, self.W2, self.b2 = W1, b1, W2, b2
 
 
-def readout_forward(x, head: DeviceReadout, stream=None):
+@_on_stream
+def readout_forward(x, head: DeviceReadout, *, stream=None):
     """(per-atom energies [N, 1], hidden features [N, Hr]) of the residual
     stream or attention output x (float32 [N, Q, C])."""
     h = linear_forward(x[:, 0], head.W1, bias=head.b1, act="silu", stream=stream)
     return linear_forward(h, head.W2, bias=head.b2, stream=stream), h
 
 
-def readout_backward(x, h, grad_e, head: DeviceReadout, stream=None):
+@_on_stream
+def readout_backward(x, h, grad_e, head: DeviceReadout, *, stream=None):
     """Gradients of sum(grad_e * e): (dL/dx [N, Q, C], zero for l > 0, and a
     dict of those of W1, b1, W2, b2); h from readout_forward."""
     torch = _torch()
     gh, gW2, gb2 = linear_backward(h, head.W2, grad_e, bias=head.b2, stream=stream)
-    with torch.cuda.stream(stream):   # None: the current stream
-        gx = torch.zeros_like(x)
+    gx = torch.zeros_like(x)
     _, gW1, gb1 = linear_backward(x[:, 0], head.W1, gh, bias=head.b1, act="silu", grad_x=gx[:, 0], stream=stream)
     return gx, dict(W1=gW1, b1=gb1, W2=gW2, b2=gb2)
 
 
-def structure_sum(values, structure, n_structures: int, stream=None):
+@_on_stream
+def structure_sum(values, structure, n_structures: int, *, stream=None):
     """Sums [n_structures] of per-atom values [N, 1] by the structure index of
     every atom (-1: the atom takes no part)."""
     return embed_backward(structure, values, n_structures, stream=stream)[:, 0]
 
 
+@_on_stream
 def model_energy(species, pos, nl: NeighborList, table, layers: List[DeviceBlockWeights], head: DeviceReadout, structure,
-                 n_structures: int, scale: float = 1.0, stream=None):
+                 n_structures: int, scale: float = 1.0, *, stream=None):
     """Energies [n_structures] from species: scaled embedding -> blocks ->
     readout -> sum over the atoms of each structure.  table float32 [V, C]."""
     Q = (layers[0].attn.L + 1) ** 2
@@ -607,8 +628,9 @@ def model_energy(species, pos, nl: NeighborList, table, layers: List[DeviceBlock
     return structure_sum(e, structure, n_structures, stream=stream)
 
 
+@_on_stream
 def attention_energy_forces(species, pos, nl: NeighborList, table, w: DeviceWeights, head: DeviceReadout, structure,
-                            n_structures: int, scale: float = 1.0, grad_energy=None, stream=None):
+                            n_structures: int, scale: float = 1.0, grad_energy=None, *, stream=None):
     """Energies, conservative forces and training gradients of the model
     species -> scaled embedding -> attention -> readout -> structure sums.
 
@@ -620,8 +642,7 @@ def attention_energy_forces(species, pos, nl: NeighborList, table, w: DeviceWeig
     o = attention_forward(x, pos, nl, w, stream=stream)
     e, h = readout_forward(o, head, stream=stream)
     energies = structure_sum(e, structure, n_structures, stream=stream)
-    with torch.cuda.stream(stream):
-        gE = torch.ones_like(energies) if grad_energy is None else grad_energy
+    gE = torch.ones_like(energies) if grad_energy is None else grad_energy
     ge = embed_forward(structure, gE.view(n_structures, 1), stream=stream)[:, :, 0]   # every atom its structure's
     go, grads = readout_backward(o, h, ge, head, stream=stream)
     gx, gp = attention_backward(x, pos, nl, w, go, stream=stream)

@@ -68,6 +68,7 @@ typedef int32_t e2f_status;
 #define E2F_I64  3
 
 #define E2F_MAX_L 6
+#define E2F_MAX_ROWS ((int64_t)0x7fffffff - 4095)   /* ids and rows of an embedding or linear call */
 
 /* Text of a status code (static storage). */
 E2F_API const char *e2f_status_string(e2f_status s);
@@ -355,8 +356,9 @@ E2F_API e2f_status e2f_embed_forward(const void *ids, int32_t id_type, int64_t N
  *               overwritten (zeros for ids that do not occur); 1: the sums
  *               are added to it.
  * The rows are sorted by id (library scratch) and summed in fp32 in an order
- * that depends on the ids alone: the result repeats bit for bit.  N <=
- * 2^31 - 1.  Fully asynchronous.
+ * that depends on the ids alone: the result repeats bit for bit.  N and V up
+ * to E2F_MAX_ROWS in both calls; no output may overlap an input.  Fully
+ * asynchronous.
  */
 E2F_API e2f_status e2f_embed_backward(const void *ids, int32_t id_type, int64_t N, const void *grad_out, int32_t dtype,
                                       int64_t V, int32_t D, float scale, int32_t Q, float *grad_table,
@@ -364,12 +366,12 @@ E2F_API e2f_status e2f_embed_backward(const void *ids, int32_t id_type, int64_t 
 
 #define E2F_ACT_NONE 0
 #define E2F_ACT_SILU 1   /* z / (1 + e^-z) */
-#define E2F_ACT_GELU 2   /* z Phi(z), Phi the normal distribution function */
+#define E2F_ACT_GELU 2   /* z Phi(z), Phi the normal distribution function to 1e-7 (absolute) */
 
 typedef struct e2f_linear {
   int32_t dtype;       /* E2F_F32 or E2F_BF16: type of x and W */
   int32_t act;         /* E2F_ACT_*: smooth ones only, so that forces are continuous */
-  int64_t M;           /* rows, 0 .. 2^31 - 1 */
+  int64_t M;           /* rows, 0 .. E2F_MAX_ROWS */
   int32_t K, N;        /* inputs and outputs, 1 .. 2^20 */
   const void *x;       /* device [M][K], row m at x + m ldx */
   int64_t ldx;         /* elements from row to row, >= K: Q C reads the l = 0 rows of [M][Q][C] in place */
@@ -385,9 +387,10 @@ typedef struct e2f_linear {
  *             may be `out` itself with ldr = ldo.
  *   out       device [M][N], row stride ldo >= N, `out_dtype` (either type
  *             for either dtype); elements between the rows are left alone.
- * bf16 products are accumulated in fp32; E2F_F32 products are those of an
- * fp32 multiply-add (tensor cores, three bf16 terms per operand).  The sum,
- * bias, activation and residual are formed in fp32 and rounded once.
+ * bf16 products are accumulated in fp32; E2F_F32 products are as accurate
+ * as fp32 multiply-adds (which small ones are; the others take three bf16 terms
+ * per operand on the tensor cores).  The sum, bias, activation and residual are
+ * formed in fp32 and rounded once.
  * Pointers need only their element's alignment, strides any value (16-byte
  * aligned pointers and rows run fastest).  out may overlap no input but the
  * residual.  Fully asynchronous.
@@ -407,7 +410,9 @@ E2F_API e2f_status e2f_linear_forward(const e2f_linear *p, const void *residual,
  * dz W, grad_W = dz^T x, grad_bias = the column sums of dz (fp32).  For
  * E2F_BF16 dz is rounded to bf16 as an operand of the products.  All outputs
  * are fully overwritten (M = 0: grad_W and grad_bias are zeros) and repeat
- * bit for bit.  No output may overlap an input.  Fully asynchronous.
+ * bit for bit.  No output may overlap an input or another output.  A row of
+ * zeros in grad_out adds nothing as long as its row of x is finite (0 * inf is
+ * NaN here too).  Fully asynchronous.
  */
 E2F_API e2f_status e2f_linear_backward(const e2f_linear *p, const void *grad_out, int64_t ldg, int32_t out_dtype,
                                        void *grad_x, int64_t ldgx, void *grad_W, int64_t ldgw, float *grad_bias,

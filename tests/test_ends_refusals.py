@@ -108,3 +108,29 @@ def test_linear_binding():
                 lambda: b(x, W, dy, grad_x=torch.zeros(4, 9)), lambda: b(x, W, dy, grad_W=torch.zeros(6, 8).bfloat16())):
         with pytest.raises(ValueError):
             bad()
+
+
+def test_limits_and_aliases(lib):
+    """More rows than E2F_MAX_ROWS (tile counts are formed as rows + tile - 1 in
+    32 bits), outputs that are an input or another output."""
+    top = (1 << 31) - 4096
+    d, o = D64, ctypes.c_void_p(4096)
+    ef = lambda N=4, V=9, out=o: lib.e2f_embed_forward(d, 2, N, ctypes.c_void_p(128), 0, V, 8, 1.0, 1, out, 0, None)
+    eb = lambda N=4, V=9, out=o: lib.e2f_embed_backward(d, 2, N, ctypes.c_void_p(128), 0, V, 8, 1.0, 1, out, 0, None)
+    for call in (ef, eb):
+        assert call(N=top + 1) == 1 and call(V=top + 1) == 1
+        assert call(out=d) == 1 and call(out=ctypes.c_void_p(128)) == 1
+    assert lib.e2f_linear_forward(_lin(M=top + 1), None, 6, o, 6, 0, None) == 1
+    assert lib.e2f_linear_forward(_lin(bias=4096), None, 6, o, 6, 0, None) == 1
+    b = lambda p, gx, gw, gb: lib.e2f_linear_backward(p, ctypes.c_void_p(512), 6, 0, gx, 8, gw, 8, gb, None)
+    assert b(_lin(M=top + 1), o, None, None) == 1
+    assert b(_lin(), o, o, None) == 1 and b(_lin(), o, None, o) == 1 and b(_lin(), None, o, o) == 1
+
+
+def test_stream_is_a_keyword():
+    """The calls make `stream` current while they allocate: it must reach them by name."""
+    ids, table, x, W = torch.zeros(4, dtype=torch.int64), torch.zeros(5, 6), torch.zeros(4, 8), torch.zeros(6, 8)
+    with pytest.raises(TypeError):
+        e2f.embed_forward(ids, table, 1.0, 1, None, None, None)
+    with pytest.raises(TypeError):
+        e2f.linear_forward(x, W, None, None, "none", None, None, None)

@@ -138,3 +138,59 @@ def test_blocks_between_the_ends(cuda_ok):
     Er = np.array([e[structure == k].sum() for k in range(2)])
     tol = 1e-4 * max(np.abs(e[structure == k]).sum() + 1 for k in range(2))
     assert np.max(np.abs(E.double().cpu().numpy() - Er)) <= tol
+
+
+def test_given_stream(cuda_ok):
+    """stream=s with another stream current: the results of the same call on the
+    current stream, in memory that belongs to s (so that neither pending work of
+    other streams nor their later allocations meet it), and so the intermediates:
+    nothing is allocated for the current stream."""
+    import torch
+    from atomistic_mlip_b200 import e2f
+    wl, species, structure, table, head = _system()
+    pos, sp, st, tab = _dev(wl.pos, species, structure, table)
+    dw = e2f.DeviceWeights.from_workload(wl, "cuda", "fp32")
+    dh = e2f.DeviceReadout(*_dev(*head))
+    nl = e2f.build_neighbors(pos, None, wl.r_c)
+    ids, tb = torch.arange(3000, device="cuda") % 50, torch.randn(50, 64, device="cuda")
+    go = torch.randn(3000, 64, device="cuda")
+
+    def run(stream):
+        E, F, g = e2f.attention_energy_forces(sp, pos, nl, tab, dw, dh, st, 2, stream=stream)
+        y = e2f.embed_forward(ids, tb, stream=stream)[:, 0]
+        gt = e2f.embed_backward(ids, go, 50, stream=stream)
+        z = e2f.linear_forward(y, tb, act="gelu", stream=stream)
+        return [E, F, gt, z, *e2f.linear_backward(y, tb, z, act="gelu", stream=stream)[:2], *(g[k] for k in sorted(g))]
+
+    want = run(None)
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    here = torch.cuda.current_stream().cuda_stream
+
+    def held(stream):   # bytes of the blocks handed out for a stream
+        return sum(seg["allocated_size"] for seg in torch.cuda.memory_snapshot() if seg["stream"] == stream)
+
+    before = held(here)
+    got = run(s)
+    assert held(here) == before
+    s.synchronize()
+    for w, t in zip(want, got):
+        assert torch.equal(w, t) or bool(((w - t).abs() <= 1e-4 * w.abs().max()).all())   # (forces: the attention's bound)
+        own = [seg for seg in torch.cuda.memory_snapshot() if seg["address"] <= t.data_ptr() < seg["address"] + seg["total_size"]]
+        assert len(own) == 1 and own[0]["stream"] == s.cuda_stream
+    assert e2f.stream_status() == 0
+
+
+def test_tall_column_sums(cuda_ok):
+    """70 million rows of one value: more blocks of rows than a grid has in y."""
+    import torch
+    from atomistic_mlip_b200 import e2f
+    M = 70_000_001
+    x = torch.ones(M, 1, device="cuda", dtype=torch.bfloat16)
+    W = torch.full((3, 1), 0.5, device="cuda", dtype=torch.bfloat16)
+    dy = torch.ones(M, 3, device="cuda", dtype=torch.bfloat16)
+    _, _, gb = e2f.linear_backward(x, W, dy, need_x=False, need_W=False, need_bias=True)
+    # ones: a CTA's 1,024 are exact, as are partial sums below 2^24; the last steps add at most 70 terms
+    # of 2^20, each rounded by at most 2^-24 of a sum below 2^27: 70 * 2^3
+    assert bool(((gb.double() - M).abs() <= 560).all())
+    assert e2f.stream_status() == 0
