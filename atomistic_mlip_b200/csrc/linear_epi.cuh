@@ -20,7 +20,8 @@ constexpr int PLAIN = 0, ACT = 1, RES = 2, DZ = 3;
 struct Sched {
   int mt, nt, tiles, nkb, bn;   // tiles: mt * nt * splits
   int vec;                      // 16-byte rows of out and extra, N a multiple of 8
-  int fixed;                    // a CTA's tiles share their columns
+  int fixed;                    // a CTA's tiles share their columns ...
+  int dm;                       // ... and are so many rows apart
   int keep;                     // DZ: ... whose sums stay in registers
 };
 
@@ -42,6 +43,12 @@ __device__ __forceinline__ Tile tile_of(const Gemm &g, const Sched &a, int i) {
   t.kb0 = t.split * g.kper;
   t.kb1 = min(t.kb0 + g.kper, a.nkb);
   return t;
+}
+// The CTA's tile i behind the one before (tile_of's divisions were a fifth of a
+// short contraction's epilogue).
+__device__ __forceinline__ void next_tile(const Gemm &g, const Sched &a, int i, Tile *t) {
+  if (a.fixed) t->m0 += a.dm;
+  else *t = tile_of(g, a, i);
 }
 
 // A chunk's residual or dL/dout: 4 x 8 elements, bf16 in lo, fp32 in lo and hi;

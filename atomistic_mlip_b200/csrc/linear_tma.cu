@@ -137,11 +137,11 @@ __device__ __forceinline__ bool io_epilogue(const Args &a, const CUtensorMap *to
   uint64_t *xbar = xbars + ew * NB;
   const int sw = (lane >> 1) & 3;   // swizzle of this lane's row
   // lane 0's loads of the extra operand: next tile, chunk and buffer
+  Tile t = tile_of(a.g, a.s, blockIdx.x), pt = t;
   int pi = blockIdx.x, pc = 0, pb = 0;
   auto load_next = [&] {
-    for (; pi < a.s.tiles; pi += gridDim.x, pc = 0) {
-      const Tile t = tile_of(a.g, a.s, pi);
-      const int n = t.n0 + cols + 32 * pc, m = t.m0 + 32 * quarter;
+    while (pi < a.s.tiles) {
+      const int n = pt.n0 + cols + 32 * pc, m = pt.m0 + 32 * quarter;
       if (pc < NCH && n < a.g.N && m < a.g.M) {
         mbar_arrive_expect_tx(&xbar[pb], IO_BUF);
         tma_load_2d(buf + pb * IO_BUF, tx, n, m, &xbar[pb]);
@@ -149,6 +149,9 @@ __device__ __forceinline__ bool io_epilogue(const Args &a, const CUtensorMap *to
         if (++pb == NB) pb = 0;
         return;
       }
+      pi += gridDim.x;
+      pc = 0;
+      if (pi < a.s.tiles) next_tile(a.g, a.s, pi, &pt);
     }
   };
   if (EXTRA && lane == 0) {
@@ -162,7 +165,7 @@ __device__ __forceinline__ bool io_epilogue(const Args &a, const CUtensorMap *to
   for (int k = 0; k < NCH; ++k) sum[k] = 0.f;
   bool ok = true;
   for (int i = blockIdx.x; i < a.s.tiles && ok; i += gridDim.x) {
-    const Tile t = tile_of(a.g, a.s, i);
+    if (i != (int)blockIdx.x) next_tile(a.g, a.s, i, &t);
     const int nw = t.n0 + cols, mw = t.m0 + 32 * quarter;
     if (EPI != PLAIN && nw != bias_of) {   // a CTA's tiles mostly share their columns
       bias_of = nw;
@@ -256,7 +259,7 @@ __device__ __forceinline__ bool io_epilogue(const Args &a, const CUtensorMap *to
   }
   if (lane == 0) stores_done();
   if (EPI == DZ && a.s.keep && e.colpart) {   // row (CTA among those of its columns, quarter)
-    const int n0 = tile_of(a.g, a.s, blockIdx.x).n0 + cols;
+    const int n0 = t.n0 + cols;
     float *row = e.colpart + (size_t)((int)blockIdx.x / a.s.nt * 4 + quarter) * a.g.N;
 #pragma unroll
     for (int k = 0; k < NCH; ++k)
@@ -309,16 +312,16 @@ gemm_tma_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ 
   if (LONGK && warp < 4) asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
   if (warp == 0) {
     if (lane == 0) {
+      Tile t = tile_of(a.g, a.s, blockIdx.x);
       int s = 0;
       uint32_t ph = 1;   // the first pass over the ring finds it empty
       bool ok = true;
       if (bres) {
-        const Tile t = tile_of(a.g, a.s, blockIdx.x);
         mbar_arrive_expect_tx(bfull, bres);
         for (int kb = 0; kb < t.kb1; ++kb) load_slice<BMN, BN>(smem + kb * BBYTES, &tbm, t.n0, kb * BK, bfull);
       }
       for (int i = blockIdx.x; i < a.s.tiles && ok; i += gridDim.x) {
-        const Tile t = tile_of(a.g, a.s, i);
+        if (i != (int)blockIdx.x) next_tile(a.g, a.s, i, &t);
         for (int kb = t.kb0; kb < t.kb1; ++kb) {
           ok = mbar_wait(&empty[s], ph, LIMIT);
           if (!ok) break;
@@ -332,11 +335,12 @@ gemm_tma_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ 
     }
   } else if (warp == 1) {
     if (lane == 0) {
+      Tile t = tile_of(a.g, a.s, blockIdx.x);
       int s = 0, u = 0;   // ring slot, accumulator units issued
       uint32_t ph = 0;
       bool ok = !bres || mbar_wait(bfull, 0, LIMIT);
       for (int i = blockIdx.x; i < a.s.tiles && ok; i += gridDim.x) {
-        const Tile t = tile_of(a.g, a.s, i);
+        if (i != (int)blockIdx.x) next_tile(a.g, a.s, i, &t);
         const int nb = min(BN, (a.g.N - t.n0 + 15) & ~15);
         const uint32_t id = idesc_bf16(128, nb, AMN, BMN);
         for (int kc = t.kb0; kc < t.kb1 && ok; kc += LONGK ? KCHUNK : t.kb1 - t.kb0, ++u) {
@@ -384,8 +388,9 @@ gemm_tma_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ 
         for (int j = 0; j < 4; ++j) sums[k][j] = both(0.f);
     }
     bool ok = true;
+    Tile t = tile_of(a.g, a.s, blockIdx.x);
     for (int i = blockIdx.x; i < a.s.tiles && ok; i += gridDim.x) {
-      const Tile t = tile_of(a.g, a.s, i);
+      if (i != (int)blockIdx.x) next_tile(a.g, a.s, i, &t);
       const int nw = t.n0 + cols, mw = t.m0 + 32 * quarter;
       const Rows rw = rows_of(a.g, t.split, mw, lane);
       if (EPI != PLAIN && nw != bias_of) {   // a CTA's tiles mostly share their columns
@@ -482,7 +487,7 @@ gemm_tma_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ 
       }
     }
     if (EPI == DZ && a.s.keep && e.colpart) {   // row (CTA among those of its columns, quarter)
-      const int n0 = tile_of(a.g, a.s, blockIdx.x).n0 + cols;
+      const int n0 = t.n0 + cols;
       float *row = a.g.e.colpart + (size_t)((int)blockIdx.x / a.s.nt * 4 + quarter) * a.g.N;
 #pragma unroll
       for (int k = 0; k < NCH; ++k)
@@ -597,6 +602,7 @@ e2f_status gemm_tma(const Gemm &g, int splits, int bn, int sms, cudaStream_t s, 
   if (even > 0 && (a.s.tiles + even - 1) / even == (a.s.tiles + a.grid - 1) / a.grid) {
     a.grid = even;
     a.s.fixed = 1;
+    a.s.dm = even / a.s.nt * 128;
     if (g.e.mode == MODE_DZ && a.s.vec) {
       a.s.keep = 1;
       if (rows_out) *rows_out = even / a.s.nt * 4;
