@@ -87,11 +87,11 @@ template <bool MN> __device__ __forceinline__ uint64_t slice_desc(uint32_t saddr
 // 512: 80 % of their peak): per chunk 32 for the accumulators, 16 in, 16 out, 8
 // for the bias.  Rows of 64 bytes, 64-byte swizzle.
 constexpr int IO_BUF = 2048;
-template <int EPI> constexpr int io_bufs() { return EPI >= RES ? 3 : 2; }
-template <int EPI> constexpr int io_ring() { return EPI >= RES ? 126976 : 147456; }
+template <int EPI, int BN> constexpr int io_bufs() { return EPI >= RES ? 3 : BN / 128; }   // (a chunk or two of a tile)
+template <int EPI, int BN> constexpr int io_ring() { return EPI >= RES ? 126976 : BN == 256 ? 147456 : 180224; }
 constexpr int IO_SBIAS = 16 * 64 * 4;
-template <int EPI> constexpr size_t io_smem() {
-  return io_ring<EPI>() + 16 * io_bufs<EPI>() * IO_BUF + IO_SBIAS + 256 + 16 * io_bufs<EPI>() * 8 + 1024;
+template <int EPI, int BN> constexpr size_t io_smem() {
+  return io_ring<EPI, BN>() + 16 * io_bufs<EPI, BN>() * IO_BUF + IO_SBIAS + 256 + 16 * io_bufs<EPI, BN>() * 8 + 1024;
 }
 
 __device__ __forceinline__ void tma_store_2d(const CUtensorMap *map, const void *src, int x, int y) {
@@ -127,7 +127,7 @@ __device__ __forceinline__ bool io_epilogue(const Args &a, const CUtensorMap *to
                                             uint32_t tmem, int ew, int lane) {
   using namespace tc;
   constexpr uint32_t LIMIT = 1u << 26;
-  constexpr int BW = BN / 4, NCH = BW / 32, NB = io_bufs<EPI>();
+  constexpr int BW = BN / 4, NCH = BW / 32, NB = io_bufs<EPI, BN>();
   constexpr bool EXTRA = EPI >= RES;
   const Epi &e = a.g.e;
   const int quarter = ew & 3, cols = (ew >> 2) * BW;
@@ -228,7 +228,7 @@ __device__ __forceinline__ bool io_epilogue(const Args &a, const CUtensorMap *to
           load_next();
         }
       } else {
-        if (lane == 0) stores_read<1>();
+        if (lane == 0) stores_read<NB - 1>();
         __syncwarp();
       }
 #pragma unroll
@@ -274,7 +274,7 @@ gemm_tma_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ 
                 const __grid_constant__ CUtensorMap to, const __grid_constant__ CUtensorMap tx,
                 const __grid_constant__ Args a) {
   using namespace tc;
-  constexpr int RING = IO ? io_ring<EPI>() : ring<EW>(), STAGING = IO ? 16 * io_bufs<EPI>() * IO_BUF : staging<EW>(),
+  constexpr int RING = IO ? io_ring<EPI, BN>() : ring<EW>(), STAGING = IO ? 16 * io_bufs<EPI, BN>() * IO_BUF : staging<EW>(),
                 SBIAS = IO ? IO_SBIAS : sbias<EW>();
   constexpr int ABYTES = BM * BK * 2, BBYTES = BN * BK * 2;
   constexpr uint32_t LIMIT = 1u << 26;
@@ -296,7 +296,7 @@ gemm_tma_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ 
     for (int i = 0; i < 2; ++i) { mbar_init(&tfull[i], 1); mbar_init(&tempty[i], EW); }
     mbar_init(bfull, 1);
     if (IO && EPI >= RES)
-      for (int i = 0; i < 16 * io_bufs<EPI>(); ++i) mbar_init(&xbar[i], 1);
+      for (int i = 0; i < 16 * io_bufs<EPI, BN>(); ++i) mbar_init(&xbar[i], 1);
     mbar_fence_init();
   }
   __syncthreads();
@@ -535,10 +535,11 @@ static bool encode(CUtensorMap *m, const void *p, long long rows, long long cols
 template <bool AMN, bool BMN, int BN, bool LONGK, int EPI, int EW, bool IO>
 static e2f_status launch_epi(const CUtensorMap &ta, const CUtensorMap &tb, Args a, cudaStream_t s) {
   // B stays in shared memory for the launch where every CTA has one column tile
-  // and three stages of A fit beside it.
-  constexpr int RING = IO ? io_ring<EPI>() : ring<EW>();
+  // and five stages of A fit beside it (with three, too few bytes in flight:
+  // 100,002 x 512 -> 128 33 us, 30 with B in the ring).
+  constexpr int RING = IO ? io_ring<EPI, BN>() : ring<EW>();
   const long long bres = (long long)a.s.nkb * BN * BK * 2, abytes = BM * BK * 2;
-  a.bres = EW == 16 && a.s.fixed && a.g.kper == a.s.nkb && bres + 3 * abytes <= RING ? (int)bres : 0;
+  a.bres = EW == 16 && a.s.fixed && a.g.kper == a.s.nkb && bres + 5 * abytes <= RING ? (int)bres : 0;
   a.st = std::min<int>(MAX_ST, (RING - a.bres) / (a.bres ? (int)abytes : stage_bytes<BN>()));
   CUtensorMap to{}, tx{};
   if (IO) {
@@ -550,7 +551,7 @@ static e2f_status launch_epi(const CUtensorMap &ta, const CUtensorMap &tb, Args 
     }
   }
   constexpr auto k = gemm_tma_kernel<AMN, BMN, BN, LONGK, EPI, EW, IO>;
-  constexpr size_t smem = IO ? io_smem<EPI>() : smem_bytes<EW>();
+  constexpr size_t smem = IO ? io_smem<EPI, BN>() : smem_bytes<EW>();
   E2F_CUDA_TRY(allow_smem<k>(smem, LONGK ? 168 : 0));
   E2F_LIN_LAUNCH(a.g, k, a.grid, threads<EW>(), smem, s, ta, tb, to, tx, a);
   return E2F_OK;
