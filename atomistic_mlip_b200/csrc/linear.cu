@@ -34,7 +34,7 @@ template <typename T, bool AMN, bool BMN> e2f_status gemm_reg(const Gemm &g, int
 template <typename T> e2f_status gemm_skinny(const Gemm &g, cudaStream_t s, int *rows_out);
 
 // linear_small.cu
-bool small_fit(int M, int N, int K, int dtype);
+bool small_fit(int M, int N, int K, int dtype, bool tma, bool extra);
 bool small_grads_fit(int M, int N, int K, int dtype);
 template <typename T> e2f_status gemm_small(const Gemm &g, cudaStream_t s);
 template <typename T>
@@ -176,9 +176,10 @@ template <bool AMN, bool BMN> struct Path<__nv_bfloat16, AMN, BMN> {
 // A product with its epilogue.  rows_out: row blocks written to e.colpart.
 template <typename T, bool AMN, bool BMN>
 static e2f_status run_gemm(Gemm g, cudaStream_t s, int *rows_out = nullptr) {
+  const bool tma = Path<T, AMN, BMN>::tma(g);
   if constexpr (!AMN && !BMN) {
     if (g.M <= 2 || g.N <= 2) return gemm_skinny<T>(g, s, rows_out);
-    if (small_fit(g.M, g.N, g.K, sizeof(T) == 4 ? E2F_F32 : E2F_BF16)) {
+    if (small_fit(g.M, g.N, g.K, sizeof(T) == 4 ? E2F_F32 : E2F_BF16, tma, g.e.extra && g.N % 8 == 0)) {
       if (rows_out) *rows_out = (g.M + 31) / 32;
       return gemm_small<T>(g, s);
     }
@@ -194,7 +195,6 @@ static e2f_status run_gemm(Gemm g, cudaStream_t s, int *rows_out = nullptr) {
   if (tiles < sms && nkb >= 16) splits = (int)std::min<long long>(sms / tiles, nkb / 4);
   g.kper = (nkb + splits - 1) / splits;
   splits = (nkb + g.kper - 1) / g.kper;
-  const bool tma = Path<T, AMN, BMN>::tma(g);
   int bn = BN;
   if (tma && g.N > BN && splits == 1) {
     // TMA path: 128 x 256 tiles feed the tensor core at its full rate; 128 x

@@ -156,13 +156,28 @@ template <typename T> __global__ void __launch_bounds__(NT) small_grads_kernel(c
 
 }  // namespace small
 
-// Contractions of up to 512 steps (128 with bf16 operands, which the tensor core
-// takes as they are), and no more pieces than the device holds at once.
-static bool fits(int rows, int cols, int k, int dtype) {
-  return k <= (dtype == E2F_F32 ? 512 : 128) && (long long)((rows + 31) / 32) * ((cols + 31) / 32) <= 1184;
+// Pieces of the output, contraction steps and their product (what a CTA slot works
+// through) up to limits.
+static bool fits(int rows, int cols, int k, int kmax, long long pieces, long long work) {
+  const long long p = (long long)((rows + 31) / 32) * ((cols + 31) / 32);
+  return k <= kmax && p <= pieces && p * k <= work;
 }
-bool small_fit(int M, int N, int K, int dtype) { return fits(M, N, K, dtype); }
-bool small_grads_fit(int M, int N, int K, int dtype) { return fits(M, K, N, dtype) && fits(N, K, M, dtype); }
+// Against the kernels with operands through registers (kernel times, fp32, SiLU):
+// 64 pieces of 64 steps 4.7 and 8.0 us, 256 of 128 8 and 9.6, 128 of 256 9.8 and
+// 12; behind the limits 512 of 128 12.5 and 9.7, 1,024 of 16 and a residual 12.5 and
+// 9.6, 128 of 512 16 and 17, with a residual 19 and 18.  Against those fed by TMA
+// (tma): 128 pieces of 16 steps 4.3 and 5.5 us, of 64 5.6 and 5.5, with a residual
+// or dL/dout on vector rows (extra) of 16 6.5 and 5.7.
+bool small_fit(int M, int N, int K, int dtype, bool tma, bool extra) {
+  if (tma) return !extra && fits(M, N, K, 32, 256, 32768);
+  return fits(M, N, K, dtype == E2F_F32 ? 256 : 128, 512, 32768);
+}
+// One launch for three: up to larger products (256 x 64 -> 128 fp32 with its dz 14
+// and 35 us).
+bool small_grads_fit(int M, int N, int K, int dtype) {
+  const int kmax = dtype == E2F_F32 ? 512 : 128;
+  return fits(M, K, N, kmax, 512, 65536) && fits(N, K, M, kmax, 512, 65536);
+}
 
 template <typename T> e2f_status gemm_small(const Gemm &g, cudaStream_t s) {
   const int grid = (g.M + 31) / 32 * ((g.N + 31) / 32);
