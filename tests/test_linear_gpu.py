@@ -353,3 +353,28 @@ def test_extreme_preactivations(cuda_ok, dt, ot):
             _check_forward(out[:, keep], x, W[keep], None, None, act)
             assert bool((out[:, 5] == float("inf")).all()) and bool(torch.isnan(out[:, 6]).all())
             assert bool(torch.isnan(out[:, 8]).all())
+
+
+@pytest.mark.parametrize("M,K,N", [(20000, 1, 37), (20011, 2, 96), (4000, 4, 513), (3001, 5, 2000), (2500, 8, 300),
+                                   (33000, 13, 132), (700, 16, 1030), (129, 16, 20000)])
+@pytest.mark.parametrize("dt,ot", TYPES)
+def test_few_inputs(cuda_ok, M, K, N, dt, ot):
+    """Up to 16 inputs and many results: rows that are and are not whole 16-byte
+    pieces, more blocks of rows than CTAs, and the same inside wider buffers."""
+    import torch
+    from atomistic_mlip_b200 import e2f
+    dt, ot = getattr(torch, dt), getattr(torch, ot)
+    x, W, b, g = _make(M, K, N, 1, dt, M + 3 * K + N)
+    r = torch.randn(M, N, generator=g, device="cuda").to(ot)
+    for pad in (0, 3):
+        if pad:
+            wide = lambda t: torch.nn.functional.pad(t, (pad, 2))[:, pad:-2]
+            x, W, r = wide(x), wide(W), wide(r)
+        for act, resid in (("silu", None), ("gelu", r)):
+            out = torch.full((M + 1, N + pad), 7.0, device="cuda", dtype=ot)
+            e2f.linear_forward(x, W, bias=b, residual=resid, act=act, out=out[:M, :N])
+            _check_forward(out[:M, :N], x, W, b, resid, act)
+            assert bool((out[M] == 7).all()) and bool((out[:, N:] == 7).all())
+        grads = e2f.linear_backward(x, W, r, bias=b, act="silu")
+        _check_backward(*grads, x, W, b, r, "silu")
+    assert e2f.stream_status() == 0
