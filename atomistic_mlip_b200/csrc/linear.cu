@@ -6,8 +6,8 @@
 //              dz = dy act'(z),  dx = dz W,  dW = dz^T x,  db = sum_m dz
 //
 // Products run on the tensor cores (linear_tma.cu, linear_reg.cu), but for those
-// with one or two rows or outputs (linear_skinny.cu) and those too small to fill
-// them (linear_small.cu).  bf16 operands are used as they are, fp32
+// with one or two rows or outputs (linear_skinny.cu), up to 16 inputs
+// (linear_thin.cu) or too few tiles to fill them (linear_small.cu).  bf16 operands are used as they are, fp32
 // accumulation.  fp32 operands are split into three bf16 terms each,
 // x = h + m + l (8 + 8 + 8 significant bits: exact), and the products
 // h h', (h m' + m h' + h l' + l h' + m m') are summed in two accumulators; the

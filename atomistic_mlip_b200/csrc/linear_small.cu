@@ -2,7 +2,7 @@
 // core's kernels nothing but their latency (8 to 10 us with fp32 operands).  A CTA
 // has a 32 x 32 piece (fp32 multiply-add, 32 contraction steps at a time, the next
 // ones on their way); shared-memory reads bound it, at a third of the fp32 rate.
-//   small_kernel        x W^T with its epilogue (forward, dz)
+//   small_kernel        x W^T with its epilogue (forward, dz; 3,000 x 128 -> 64 7.8 us)
 //   small_grads_kernel  dx = dz W, dW = dz^T x and the bias's column sums in one
 //                       launch (300 x 72 x 96 fp32: 24 us a call against 36)
 #include <algorithm>

