@@ -196,7 +196,21 @@ static e2f_status run_gemm(Gemm g, cudaStream_t s, int *rows_out = nullptr) {
   const long long tiles = (long long)mt * nt;
   const int sms = sm_count();
   int splits = 1;
-  if (tiles < sms && nkb >= 16) splits = (int)std::min<long long>(sms / tiles, nkb / 4);
+  if (tiles < sms && nkb >= 16) {
+    splits = (int)std::min<long long>(sms / tiles, nkb / 4);
+    // Operands through registers cost over a microsecond a block: further splits
+    // where their rounds are shorter by more than the partial sums take (10,513 x
+    // 1,427 -> 9 fp32, 83 tiles: whole 65 us, in three 48).
+    if (!tma) {
+      auto blocks = [&](int n) {
+        const long long rounds = (tiles * n + sms - 1) / sms;
+        return (double)(rounds * ((nkb + n - 1) / n)) + (n > 1 ? 3 + 2e-6 * n * g.M * g.N : 0);
+      };
+      const int most = std::min(8, nkb / 4);
+      for (int n = splits + 1; n <= most; ++n)
+        if (blocks(n) < blocks(splits)) splits = n;
+    }
+  }
   g.kper = (nkb + splits - 1) / splits;
   splits = (nkb + g.kper - 1) / g.kper;
   int bn = BN;
