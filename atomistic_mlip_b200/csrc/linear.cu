@@ -13,8 +13,8 @@
 // h h', (h m' + m h' + h l' + l h' + m m') are summed in two accumulators; the
 // terms left out are below 2^-24 of a product, so the result is that of an
 // fp32 product at six bf16 products' cost (nominal 375 TFLOP/s against 74 on
-// the CUDA cores).  A product that meets an infinity gives NaN in the split
-// form (inf * 0); such elements are summed again from the fp32 operands.
+// the CUDA cores).  Infinities and NaN take part by their h alone: where the sum of
+// h h' is not finite it is the result, at no cost of time.
 #include <algorithm>
 
 #include "linear.cuh"

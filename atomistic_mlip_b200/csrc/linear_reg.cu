@@ -91,7 +91,15 @@ __device__ __forceinline__ void load8(Raw<float> &r, const float *p, int nv, boo
 
 // Terms of a chunk to shared memory, TILE_BYTES apart.
 __device__ __forceinline__ void put8(const Raw<__nv_bfloat16> &r, uint8_t *p) { *reinterpret_cast<uint4 *>(p) = r.a; }
+// The terms of half the value: the largest fp32 values do not round to a bf16
+// infinity so.  (4,096 x 4,096 -> 2,048: 405 us without the halving, 409 with it, 440
+// if they are told apart instead.)  Infinities and NaN have themselves as h; their m
+// and l are NaN, which join() below leaves out.
+constexpr float SPLIT_SCALE = 4.f;   // of a product of two such sums
 __device__ __forceinline__ void split2(float x, float y, uint32_t &h, uint32_t &m, uint32_t &l) {
+  const f2 half = mul2({x, y}, both(0.5f));
+  x = half.x;
+  y = half.y;
   h = pack_bf16x2(x, y);
   x -= __uint_as_float(h << 16);
   y -= __uint_as_float(h & 0xffff0000u);
@@ -110,6 +118,11 @@ __device__ __forceinline__ void put8(const Raw<float> &r, uint8_t *p) {
   *reinterpret_cast<uint4 *>(p + TILE_BYTES) = m;
   *reinterpret_cast<uint4 *>(p + 2 * TILE_BYTES) = l;
 }
+
+// The sum of h h' and that of the smaller products.  Where the first is not
+// finite it is the result: the infinities and NaN of the operands are in it as in an
+// fp32 product.
+__device__ __forceinline__ float join(float hh, float small) { return fabsf(hh) < INFINITY ? hh + small : hh; }
 
 // The chunks of one operand tile this thread carries: rows r0 .. (m or n) below
 // RN, contraction k0 .. below KN.
@@ -131,17 +144,6 @@ template <typename T, bool MN> __device__ __forceinline__ void put_tile(const Ra
     const int q = threadIdx.x + CONV * j;
     if ((MN ? 8 * (q & 15) : q >> 3) < nb) put8(r[j], s + chunk_off<MN>(q));
   }
-}
-
-// An element of the product from the fp32 operands themselves.
-template <bool AMN, bool BMN>
-__device__ __noinline__ float dot_again(const Gemm &g, int m, int n, int k0, int k1) {
-  const float *A = static_cast<const float *>(g.A), *B = static_cast<const float *>(g.B);
-  float s = 0.f;
-  for (int k = k0; k < k1; ++k)
-    s = fmaf(AMN ? A[(size_t)(k * g.lda) + m] : A[(size_t)(m * g.lda) + k],
-             BMN ? B[(size_t)(k * g.ldb) + n] : B[(size_t)(n * g.ldb) + k], s);
-  return s;
 }
 
 // Registers: 16 carrying warps 64, four control warps 24, eight epilogue warps
@@ -290,7 +292,7 @@ __global__ void __launch_bounds__(NT, 1) gemm_reg_kernel(const __grid_constant__
             if (NS == 3) {
               tmem_ld_32x32b_x16(ta + 128, v);
 #pragma unroll
-              for (int j = 0; j < 16; ++j) acc[c + j] += v[j];
+              for (int j = 0; j < 16; ++j) acc[c + j] = join(acc[c + j], v[j]);
             }
           }
           tc_fence_before();
@@ -312,28 +314,32 @@ __global__ void __launch_bounds__(NT, 1) gemm_reg_kernel(const __grid_constant__
                            [&](int h, float (&v)[16]) {
           if constexpr (LONGK) {
 #pragma unroll
-            for (int j = 0; j < 16; ++j) v[j] = acc[16 * h + j];
+            for (int j = 0; j < 16; ++j) v[j] = NS == 3 ? SPLIT_SCALE * acc[16 * h + j] : acc[16 * h + j];
           } else {
             const uint32_t ta = tq + (u & 1) * ACC + cc + 16 * h;
             tmem_ld_32x32b_x16(ta, v);
             if (NS == 3) {
               float w[16];
               tmem_ld_32x32b_x16(ta + 128, w);
+              float z = 0.f;   // 0 * v is NaN for infinities and NaN
 #pragma unroll
-              for (int j = 0; j < 16; ++j) v[j] += w[j];
+              for (int j = 0; j < 16; ++j) {
+                v[j] += w[j];
+                z = fmaf(0.f, v[j], z);
+                v[j] *= SPLIT_SCALE;
+              }
+              if (__any_sync(0xffffffffu, z != z)) {   // (four at a time: 16 spill)
+#pragma unroll
+                for (int j = 0; j < 16; j += 4) {
+                  uint32_t hh[4], sm[4];
+                  tmem_ld_cols<4>(ta + j, hh);
+                  tmem_ld_cols<4>(ta + 128 + j, sm);
+#pragma unroll
+                  for (int k = 0; k < 4; ++k)
+                    v[j + k] = SPLIT_SCALE * join(__uint_as_float(hh[k]), __uint_as_float(sm[k]));
+                }
+              }
             }
-          }
-          if (NS == 3) {   // 0 * v is NaN for infinities and NaN
-            float z = 0.f;
-#pragma unroll
-            for (int j = 0; j < 16; ++j) z = fmaf(0.f, v[j], z);
-            if (z != z && mw + lane < g.M) {
-#pragma unroll
-              for (int j = 0; j < 16; ++j)
-                if (v[j] != v[j] && n + 16 * h + j < g.N)
-                  v[j] = dot_again<AMN, BMN>(g, mw + lane, n + 16 * h + j, t.kb0 * BK, min(t.kb1 * BK, g.K));
-            }
-            __syncwarp();
           }
         });
         if constexpr (LONGK) {   // the next chunk's sums to the front: no index that depends on c

@@ -1,0 +1,113 @@
+"""Linear layers where their kernels' number formats end: infinities and NaN, the
+largest and the smallest fp32 values."""
+import pytest
+
+from .test_linear_gpu import _acc
+
+pytestmark = pytest.mark.gpu
+
+# fp32 products of tiles on the tensor cores, in all three operand orders: short
+# contractions, split ones, and chains of more than 1,024
+TILED = [(600, 300, 520), (40, 2000, 150), (1600, 1200, 1100)]
+
+
+def _same(got, ref, tol):
+    """NaN, +inf and -inf where ref has them; elsewhere within tol."""
+    import torch
+    fine = torch.isfinite(ref)
+    assert torch.equal(torch.isnan(got), torch.isnan(ref))
+    assert torch.equal(got == float("inf"), ref == float("inf"))
+    assert torch.equal(got == float("-inf"), ref == float("-inf"))
+    assert bool(((got.double() - ref).abs() <= tol)[fine].all())
+
+
+def _plant(t, rows):
+    inf, nan = float("inf"), float("nan")
+    t[rows[0], 3] = inf
+    t[rows[1], 7] = nan
+    t[rows[2], 0], t[rows[2], t.shape[1] - 1] = -inf, inf
+    t[rows[3], 11] = -inf
+
+
+@pytest.mark.parametrize("M,K,N", TILED)
+def test_infinities_and_nan_of_both_operands(cuda_ok, M, K, N):
+    """They reach the outputs that an fp32 multiply-add gives them, and no others."""
+    import torch
+    from atomistic_mlip_b200 import e2f
+    g = torch.Generator(device="cuda")
+    g.manual_seed(M)
+    x = torch.randn(M, K, generator=g, device="cuda")
+    W = torch.randn(N, K, generator=g, device="cuda")
+    dy = torch.randn(M, N, generator=g, device="cuda")
+    r = torch.randn(M, N, generator=g, device="cuda")
+    W[5, 3] = dy[1, 4] = 0.0                 # inf * 0
+    _plant(x, (1, 2, 17, M - 1))
+    _plant(W, (N - 1, 20, 33, 64))
+    x8, W8, dy8 = x.double(), W.double(), dy.double()
+    _same(e2f.linear_forward(x, W), x8 @ W8.t(), 1.01 * _acc(K) * (x8.abs() @ W8.abs().t()))
+    S = x8.abs() @ W8.abs().t() + r.double().abs()
+    _same(e2f.linear_forward(x, W, residual=r), x8 @ W8.t() + r.double(), 1.01 * _acc(K) * S)
+    _plant(dy, (0, 19, 30, M - 2))
+    dy8 = dy.double()
+    gx, gw, gb = e2f.linear_backward(x, W, dy, need_bias=True)
+    _same(gx, dy8 @ W8, 1.01 * _acc(N) * (dy8.abs() @ W8.abs()))
+    _same(gw, dy8.t() @ x8, 1.01 * _acc(M) * (dy8.abs().t() @ x8.abs()))
+    _same(gb, dy8.sum(0), 1.01 * _acc(M) * dy8.abs().sum(0))
+    assert e2f.stream_status() == 0
+
+
+@pytest.mark.parametrize("M,K", [(600, 600), (1600, 1200)])
+def test_values_beyond_the_bf16_range(cuda_ok, M, K):
+    """fp32 values that round to a bf16 infinity pass through a unit matrix as they
+    are, from either operand; products beyond the fp32 range are infinities."""
+    import torch
+    from atomistic_mlip_b200 import e2f
+    g = torch.Generator(device="cuda")
+    g.manual_seed(K)
+    top = 0x7f7fffff                          # the largest finite value's bits
+    bits = torch.randint(0x7f7f0000, top + 1, (M, K), generator=g, device="cuda", dtype=torch.int32)
+    x = bits.view(torch.float32) * (torch.randint(0, 2, (M, K), generator=g, device="cuda") * 2 - 1)
+    x[0] = torch.finfo(torch.float32).max
+    x[1] = -x[0]
+    eye = torch.eye(K, device="cuda")
+    assert torch.equal(e2f.linear_forward(x, eye), x)
+    assert torch.equal(e2f.linear_forward(eye, x), x.t())
+    gx, gw, _ = e2f.linear_backward(eye, x, torch.eye(K, M, device="cuda"))       # dy W, dy^T x
+    assert torch.equal(gx, torch.nn.functional.pad(x, (0, 0, 0, max(0, K - M)))[:K])
+    assert torch.equal(gw, torch.eye(M, K, device="cuda"))
+    big = torch.full((M, K), 1e30, device="cuda")
+    out = e2f.linear_forward(big, torch.full((K, K), 1.1e20, device="cuda"))
+    assert bool((out == float("inf")).all())
+    assert e2f.stream_status() == 0
+
+
+def test_nan_costs_nothing(cuda_ok):
+    """A diverged step takes no longer than another one (medians of device times; the
+    factor of three leaves room for a clock that changes between them)."""
+    import torch
+    from atomistic_mlip_b200 import e2f
+    x, W = torch.randn(1024, 1024, device="cuda"), torch.randn(512, 1024, device="cuda")
+    one, dy = x.clone(), torch.randn(1024, 512, device="cuda")
+    one[3, 5] = float("nan")
+    nan = torch.full_like(x, float("nan"))
+
+    def us(x, dy):
+        t = []
+        for _ in range(9):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            out = e2f.linear_forward(x, W)
+            gw = e2f.linear_backward(x, W, dy, need_x=False)[1]
+            b.record()
+            b.synchronize()
+            t.append(a.elapsed_time(b) * 1e3)
+        return sorted(t)[4], out, gw
+
+    usual, _, _ = us(x, dy)
+    t, out, gw = us(one, dy)
+    assert bool(torch.isnan(out[3]).all()) and int(torch.isnan(out).sum()) == 512
+    assert bool(torch.isnan(gw[:, 5]).all()) and int(torch.isnan(gw).sum()) == 512
+    assert t <= 3 * usual
+    t, out, gw = us(nan, dy)
+    assert bool(torch.isnan(out).all()) and bool(torch.isnan(gw).all()) and t <= 3 * usual
+    assert e2f.stream_status() == 0
