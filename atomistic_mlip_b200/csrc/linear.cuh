@@ -173,6 +173,8 @@ __device__ __forceinline__ void store_as(void *p, int type, size_t i, float v) {
 }
 
 // One element through the epilogue; returns what MODE_DZ adds to its column's sum.
+// (The product is rounded before it is added: fused with the addition where dz is
+// not stored as well, it would give the sums other bits there.)
 __device__ __forceinline__ float epi_elem(const Epi &e, long long m, int n, float v, float bias) {
   v += bias;
   if (e.mode == MODE_OUT) {
@@ -181,7 +183,7 @@ __device__ __forceinline__ float epi_elem(const Epi &e, long long m, int n, floa
     store_as(e.out, e.otype, (size_t)(m * e.ldo) + n, v);
     return 0.f;
   }
-  v = act_bwd(e.act, v) * load_as(e.extra, e.etype, (size_t)(m * e.lde) + n);
+  v = __fmul_rn(act_bwd(e.act, v), load_as(e.extra, e.etype, (size_t)(m * e.lde) + n));
   if (e.out) store_as(e.out, e.otype, (size_t)(m * e.ldo) + n, v);
   return v;
 }

@@ -307,7 +307,7 @@ __device__ __forceinline__ void epi_chunk(const Gemm &g, int vec, int split, con
           float w = st[r * 32 + ((((lane >> 2) ^ (r & 7)) << 2) | (lane & 3))];
           if (EXTRA) {
             const float y = __uint_as_float(x.word(r));
-            w = EPI == RES ? w + y : w * y;
+            w = EPI == RES ? w + y : __fmul_rn(w, y);
             sum += w;
           }
           if (store) {
@@ -335,7 +335,7 @@ __device__ __forceinline__ void epi_chunk(const Gemm &g, int vec, int split, con
             continue;
           }
           if (EXTRA) {
-            w = EPI == RES ? w + y[r] : w * y[r];
+            w = EPI == RES ? w + y[r] : __fmul_rn(w, y[r]);
             sum += w;
           }
           if (EPI != DZ || e.out) store_as(e.out, e.otype, (size_t)(m * e.ldo) + nl, w);
@@ -376,7 +376,9 @@ inline int epi_kind(const Epi &e) {
 // ends after KCHUNK blocks (linear_tma.cu).
 constexpr int KCHUNK = 16;
 inline bool long_chain(const Gemm &g) {
-  const bool fp32 = g.e.mode == MODE_PART || (g.e.mode == MODE_OUT ? g.e.otype == E2F_F32 : g.e.colpart != nullptr);
+  // (dz whether its column sums are asked for or not: any subset of the gradients has
+  // the bits of all of them)
+  const bool fp32 = g.e.mode != MODE_OUT || g.e.otype == E2F_F32;
   return fp32 && g.kper > KCHUNK;
 }
 

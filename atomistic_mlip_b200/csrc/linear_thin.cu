@@ -112,7 +112,7 @@ __global__ void __launch_bounds__(NT) thin_kernel(const __grid_constant__ Gemm g
         if (e.mode == MODE_DZ) {
 #pragma unroll
           for (int c = 0; c < CPL; ++c) {
-            v[c] = act_bwd(e.act, v[c]) * (EXTRA ? y[u][c] : 0.f);
+            v[c] = __fmul_rn(act_bwd(e.act, v[c]), EXTRA ? y[u][c] : 0.f);
             csum[c] += v[c];
           }
         } else {

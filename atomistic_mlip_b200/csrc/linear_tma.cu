@@ -242,7 +242,7 @@ __device__ __forceinline__ bool io_epilogue(const Args &a, const CUtensorMap *to
                                  pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
       fence_async_smem();
       __syncwarp();
-      if (lane == 0) tma_store_2d(to, buf + b * IO_BUF, n, mw);
+      if (lane == 0 && (EPI != DZ || e.out)) tma_store_2d(to, buf + b * IO_BUF, n, mw);
       if (++b == NB) { b = 0; xph ^= 1; }
       if (EPI == DZ && e.colpart) {
         const float s = transposed_sum(v, lane);
@@ -549,7 +549,7 @@ static e2f_status launch_epi(const CUtensorMap &ta, const CUtensorMap &tb, Args 
   CUtensorMap to{}, tx{};
   if (IO) {
     const Epi &e = a.g.e;
-    if (!encode(&to, e.out, a.g.M, a.g.N, e.ldo, 32, 32) ||
+    if ((e.out && !encode(&to, e.out, a.g.M, a.g.N, e.ldo, 32, 32)) ||
         (EPI >= RES && !encode(&tx, e.extra, a.g.M, a.g.N, e.lde, 32, 32))) {
       set_cuda_error(cudaErrorInvalidValue, "cuTensorMapEncodeTiled");
       return E2F_ERR_CUDA;
@@ -567,7 +567,8 @@ static e2f_status launch_kind(const CUtensorMap &ta, const CUtensorMap &tb, cons
   if constexpr (!LONGK) {
     const Epi &e = a.g.e;
     if (a.g.kper <= short_k(EPI)) {
-      const bool io = e.mode != MODE_PART && e.out && e.otype == E2F_BF16 && tma_operand(e.out, e.ldo) &&
+      // (a dz that is not stored takes the same kernel: its column sums have one order)
+      const bool io = e.mode != MODE_PART && e.otype == E2F_BF16 && (e.out ? tma_operand(e.out, e.ldo) : EPI == DZ) &&
                       (EPI < RES || (e.etype == E2F_BF16 && tma_operand(e.extra, e.lde)));
       if (io) return launch_epi<AMN, BMN, BN, false, EPI, 16, true>(ta, tb, a, s);
       return launch_epi<AMN, BMN, BN, false, EPI, 16, false>(ta, tb, a, s);

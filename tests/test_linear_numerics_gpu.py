@@ -1,8 +1,8 @@
 """Linear layers where their kernels' number formats end: infinities and NaN, the
-largest and the smallest fp32 values."""
+largest and the smallest fp32 values; and which bits may depend on what."""
 import pytest
 
-from .test_linear_gpu import _acc
+from .test_linear_gpu import TYPES, _acc, _make
 
 pytestmark = pytest.mark.gpu
 
@@ -110,4 +110,23 @@ def test_nan_costs_nothing(cuda_ok):
     assert t <= 3 * usual
     t, out, gw = us(nan, dy)
     assert bool(torch.isnan(out).all()) and bool(torch.isnan(gw).all()) and t <= 3 * usual
+    assert e2f.stream_status() == 0
+
+
+@pytest.mark.parametrize("M,K,N", [(700, 136, 520), (3000, 128, 512), (2500, 2056, 1288), (5000, 1160, 640), (1600, 1200, 1100),
+                                   (257, 2056, 130), (3000, 128, 514), (2500, 2056, 1290), (3001, 8, 100), (2, 300, 70), (130, 40, 2), (120, 72, 96), (900, 77, 130)])
+@pytest.mark.parametrize("dt,gt", TYPES)
+@pytest.mark.parametrize("act", ["silu", "gelu", "none"])
+def test_any_subset_of_the_gradients_has_the_same_bits(cuda_ok, M, K, N, dt, gt, act):
+    import torch
+    from atomistic_mlip_b200 import e2f
+    dt, gt = getattr(torch, dt), getattr(torch, gt)
+    x, W, b, g = _make(M, K, N, 1, dt, M + K + N)
+    dy = torch.randn(M, N, generator=g, device="cuda").to(gt)
+    full = e2f.linear_backward(x, W, dy, bias=b, act=act)
+    for need in ((1, 0, 0), (0, 1, 0), (0, 0, 1), (1, 1, 0), (1, 0, 1), (0, 1, 1)):
+        part = e2f.linear_backward(x, W, dy, bias=b, act=act, need_x=bool(need[0]), need_W=bool(need[1]),
+                                   need_bias=bool(need[2]))
+        for p, q, n in zip(part, full, need):
+            assert torch.equal(p, q) if n else p is None
     assert e2f.stream_status() == 0
