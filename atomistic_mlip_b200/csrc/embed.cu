@@ -32,11 +32,12 @@
 #include <algorithm>
 
 #include "common.cuh"
+#include "embed_plan.cuh"
 
 namespace e2f {
 namespace emb {
 
-constexpr int NT = 256;
+constexpr int NT = RED_NT;
 
 // VE consecutive elements of a row as floats (VE * sizeof(T) is 16, 4 or the
 // element's size; the caller guarantees that alignment).
@@ -242,8 +243,6 @@ static e2f_status pick_fwd(const I *ids, int64_t N, const T *table, int64_t V, i
 // stable radix sort of (id, row)
 // ---------------------------------------------------------------------------
 constexpr int RB = 256;          // digit values of a pass
-constexpr int SUB = 2048;        // keys a CTA ranks at a time: 8 warps x 256
-constexpr int MAX_TILES = 128;   // CTAs of a pass; longer inputs give each more keys
 
 struct SortArgs {
   int N, shift, tile;            // tile: keys per CTA, a multiple of SUB
@@ -400,20 +399,16 @@ template <int VE> __device__ __forceinline__ void write_sum(const RedArgs &a, ui
 
 // First place of the sorted keys with a key >= v, by a whole warp: 32 probes a step.
 __device__ __forceinline__ int lower_bound_warp(const uint32_t *keys, int n, uint32_t v, int lane) {
-  int lo = 0, hi = n;   // keys[lo - 1] < v <= keys[hi]
+  int lo = 0, hi = n;
   while (lo < hi) {
-    const int step = (hi - lo + 31) >> 5, p = lo + (lane + 1) * step - 1;
+    const int step = probe_step(lo, hi), p = probe_at(lo, step, lane);
     const uint32_t ge = __ballot_sync(0xffffffffu, p >= hi || keys[p] >= v);
-    const int f = ge ? __ffs(ge) - 1 : 32;   // the first probe at or behind the bound
-    hi = min(hi, lo + (f + 1) * step - 1);
-    lo = lo + f * step;
-    if (lo > hi) lo = hi;
+    narrow(lo, hi, step, ge ? __ffs(ge) - 1 : 32);
   }
   return lo;
 }
 
 // Zeros to those of the ids v0 .. v0 + ZROWS that do not occur.
-constexpr int ZROWS = 64;
 __device__ __forceinline__ void zero_absent(const RedArgs &a, long long v0, int *sm) {
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
   const int nv = (int)min((long long)ZROWS, a.V - v0);
@@ -445,8 +440,6 @@ __device__ __forceinline__ void zero_absent(const RedArgs &a, long long v0, int 
   }
 }
 
-// Resident CTAs: the tile is chosen so that one wave of them covers the rows.
-constexpr int RED_CTAS = 4;
 template <typename T, int VE>
 __global__ void __launch_bounds__(NT, RED_CTAS) reduce_kernel(RedArgs a, const T *__restrict__ g) {
   extern __shared__ int sm[];
@@ -655,12 +648,11 @@ __global__ void __launch_bounds__(32 * JG) combine_kernel(RedArgs a) {
 }
 
 template <typename T, int VE>
-static e2f_status launch_reduce(RedArgs a, const T *g, cudaStream_t s) {
+static e2f_status launch_reduce(RedArgs a, int zero, const T *g, cudaStream_t s) {
   const int dv = (a.D + VE - 1) / VE;
   const int RG = NT / a.CL;
   const size_t smem = sizeof(int) * (size_t)(2 * a.R + 2 + 2 * NT * VE + RG + a.R / 32 + 2);
-  const int zero = a.accumulate ? 0 : (a.V + ZROWS - 1) / ZROWS;
-  dim3 grid((unsigned)(a.tiles + zero), (unsigned)((dv + a.CL - 1) / a.CL));
+  dim3 grid((unsigned)a.tiles + (unsigned)zero, (unsigned)((dv + a.CL - 1) / a.CL));
   E2F_LAUNCH_AFTER((reduce_kernel<T, VE>), grid, NT, smem, s, a, g);
   if (a.tiles > 1) {
     dim3 cg((unsigned)((a.tiles - 1 + JG - 1) / JG), (unsigned)std::min(64, (a.D + 31) / 32));
@@ -850,22 +842,15 @@ static e2f_status backward(const I *ids, int64_t N64, const T *g, int64_t V, int
     if (VE == 2) return launch_small<I, T, 2>(a, ids, g, err, s);
     return launch_small<I, T, 1>(a, ids, g, err, s);
   }
-  const int dv = (D + VE - 1) / VE;
-  a.CL = 8;   // eight lanes at least: the row groups are joined one after another
-  while (a.CL < 32 && a.CL < dv) a.CL <<= 1;
-  // rows of a group: a multiple of eight (batches of loads) that lets one wave
-  // of CTAs cover everything, 32 at most (100,002 rows, D = 128: 24 rows 12 us,
-  // 16 rows, a wave and a bit, 18 us)
-  const int RG = NT / a.CL;
-  const long long cols = (dv + a.CL - 1) / a.CL, slots = 148 * RED_CTAS;
-  const int G = (int)std::min<long long>(32, 8 * (((N + 8LL * RG - 1) / (8LL * RG) * cols + slots - 1) / slots));
-  a.R = std::min(1024, RG * G);
-  a.tiles = (N + a.R - 1) / a.R;
+  const RunPlan rp = run_plan(N, V, (D + VE - 1) / VE);
+  a.CL = rp.CL;
+  a.R = rp.R;
+  a.tiles = rp.tiles;
+  const int zero = accumulate ? 0 : rp.zero;
+  const SortPlan sp = sort_plan(N, V);
   SortArgs sa{};
-  sa.N = N; sa.V = (int)V;
-  const int subs = (N + SUB - 1) / SUB, per = (subs + MAX_TILES - 1) / MAX_TILES;
-  sa.tile = per * SUB;
-  const int st = (N + sa.tile - 1) / sa.tile;
+  sa.N = N; sa.V = (int)V; sa.tile = sp.tile; sa.tiles = sp.tiles;
+  const int st = sp.tiles, passes = sp.passes;
   auto up = [](size_t b) { return (b + 255) & ~(size_t)255; };
   const size_t kb = up(sizeof(int) * (size_t)N), pb = up(sizeof(float) * (size_t)a.tiles * D);
   Scratch ws;
@@ -876,10 +861,6 @@ static e2f_status backward(const I *ids, int64_t N64, const T *g, int64_t V, int
   a.head = reinterpret_cast<float *>(w + 4 * kb);
   a.tail = reinterpret_cast<float *>(w + 4 * kb + pb);
   int *hist = reinterpret_cast<int *>(w + 4 * kb + 2 * pb);
-  // keys run over 0 .. V (V: rows that take no part)
-  int passes = 1;
-  while (8 * passes < 32 && ((uint64_t)V >> (8 * passes)) != 0) ++passes;
-  sa.tiles = st;
   E2F_LAUNCH((hist_kernel<I, true>), st, NT, 0, s, sa, ids, nullptr, hist, err);
   E2F_LAUNCH_AFTER((scatter_kernel<I, true>), st, NT, 0, s, sa, ids, nullptr, nullptr, hist, k0, q0);
   for (int pass = 1; pass < passes; ++pass) {
@@ -891,9 +872,9 @@ static e2f_status backward(const I *ids, int64_t N64, const T *g, int64_t V, int
   }
   a.keys = k0;
   a.rows = q0;
-  if (VE == W) return launch_reduce<T, W>(a, g, s);
-  if (VE == 2) return launch_reduce<T, 2>(a, g, s);
-  return launch_reduce<T, 1>(a, g, s);
+  if (VE == W) return launch_reduce<T, W>(a, zero, g, s);
+  if (VE == 2) return launch_reduce<T, 2>(a, zero, g, s);
+  return launch_reduce<T, 1>(a, zero, g, s);
 }
 
 template <typename I>
