@@ -1,5 +1,7 @@
 """Linear layers where their kernels' number formats end: infinities and NaN, the
 largest and the smallest fp32 values; and which bits may depend on what."""
+import math
+
 import pytest
 
 from .test_linear_gpu import TYPES, _acc, _make
@@ -130,3 +132,70 @@ def test_any_subset_of_the_gradients_has_the_same_bits(cuda_ok, M, K, N, dt, gt,
         for p, q, n in zip(part, full, need):
             assert torch.equal(p, q) if n else p is None
     assert e2f.stream_status() == 0
+
+
+def _through(act, z, K, M, dt, dy=None):
+    """act (or its gradient) of the values z [K], repeated in M rows, through a unit matrix."""
+    import torch
+    from atomistic_mlip_b200 import e2f
+    x = z.to(dt).repeat(M, 1)
+    eye = torch.eye(K, device="cuda").to(dt)
+    if dy is None:
+        return e2f.linear_forward(x, eye, act=act, out_dtype=torch.float32)
+    ones = torch.full((M, K), dy, device="cuda")
+    return e2f.linear_backward(x, eye, ones, act=act, need_x=False, need_W=False, need_bias=True)[2] / M
+
+
+# M, K, type: streamed rows, few inputs, the CUDA cores, fp32 and unaligned tiles, tiles by TMA
+KERNELS = [(2, 512, "float32"), (64, 16, "float32"), (64, 128, "float32"), (1024, 512, "float32"), (2048, 1280, "float32"),
+           (1024, 515, "bfloat16"), (1024, 512, "bfloat16"), (256, 1280, "bfloat16"), (2048, 1280, "bfloat16")]
+
+
+def _phi_by_formula(z):
+    """Abramowitz and Stegun 7.1.26 in 64 bits, for z < 0."""
+    import torch
+    t = 1 / (1 + 0.3275911 * z.abs() / math.sqrt(2))
+    q = 0.254829592 + t * (-0.284496736 + t * (1.421413741 + t * (-1.453152027 + t * 1.061405429)))
+    return 0.5 * t * q * torch.exp(-0.5 * z * z)
+
+
+@pytest.mark.parametrize("M,K,dt", KERNELS)
+def test_gelu_in_its_lower_tail(cuda_ok, M, K, dt):
+    """Relative to the formula that the kernels evaluate: its exponent z^2 / 2 is off by
+    3 roundings, exponential and reciprocal by 2^-22 each, the polynomial (whose terms
+    are at most 3.3 times their sum) and the products by 3.3 * 16 roundings.  Relative
+    to Phi: the formula's own 0.4 %."""
+    import torch
+    dt = getattr(torch, dt)
+    z = torch.linspace(-6.0, -3.0, K, device="cuda").to(dt).double()
+    tol = (3 * z * z / 2 + 8 + 53) * 2.0 ** -24 * 1.01
+    y = _through("gelu", z, K, M, dt)
+    assert torch.equal(y, y[:1].expand_as(y))
+    want = z * _phi_by_formula(z)
+    assert bool(((y[0].double() - want).abs() <= tol * want.abs()).all())
+    exact = 0.5 * z * torch.erfc(-z / math.sqrt(2))
+    assert bool(((y[0].double() - exact).abs() <= (4e-3 + tol) * exact.abs()).all())
+    # the gradient Phi + z phi: the column sums of dz = 1 act'(z), M equal terms
+    g = _through("gelu", z, K, M, dt, 1.0).double()
+    pdf = torch.exp(-0.5 * z * z) / math.sqrt(2 * math.pi)
+    want = _phi_by_formula(z) + z * pdf
+    mag = _phi_by_formula(z) + z.abs() * pdf
+    assert bool(((g - want).abs() <= tol * mag + (M + 2) * 2.0 ** -24 * want.abs()).all())
+
+
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_a_pre_activation_gives_the_same_bits_in_every_kernel(cuda_ok, act):
+    import torch
+    for dt in ("float32", "bfloat16"):
+        z = torch.cat([torch.linspace(-14, 14, 497), torch.tensor([0.0, -0.0, 1e-30, -1e-30, 0.5, -0.5, 88.0, -88.0, 1e4, -1e4,
+                                                                   2.0 ** -20, -2.0 ** -20, 3.0, -3.0, 1.0])]).cuda()
+        z = z.to(getattr(torch, dt)).float()
+        seen = None
+        for M, K, kd in KERNELS:
+            if kd != dt and not (dt == "bfloat16" and kd == "float32"):
+                continue
+            out = torch.cat([_through(act, torch.nn.functional.pad(zz, (0, K - zz.numel())), K, M, getattr(torch, kd))[M - 1, :zz.numel()]
+                             for zz in z.split(K)])
+            if seen is None:
+                seen = out
+            assert torch.equal(out, seen), (M, K, kd)
