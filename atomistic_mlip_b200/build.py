@@ -10,6 +10,7 @@ from __future__ import annotations
 import concurrent.futures as cf
 import glob
 import os
+import re
 import subprocess
 import sys
 
@@ -39,10 +40,40 @@ def up_to_date() -> bool:
     return all(os.path.getmtime(p) <= t for p in _deps())
 
 
-def _compile(src: str, extra) -> str:
+# Kernels that redistribute their registers (setmaxnreg), by mangled name, and the
+# registers a thread that they must be launched with to do so.
+REDISTRIBUTED = [(re.compile(r"gemm_reg_kernelI"), 72),
+                 (re.compile(r"gemm_tma_kernelILb[01]ELb[01]ELi\d+ELb1E"), 168)]   # LONGK
+
+
+def check_registers(ptxas_report: str) -> int:
+    """Number of such kernels in ptxas's report; RuntimeError if one was compiled to
+    fewer registers than it hands out (it would wait for ever)."""
+    name, seen = "", 0
+    for line in ptxas_report.splitlines():
+        m = re.search(r"Compiling entry function '([^']+)'", line)
+        if m:
+            name = m.group(1)
+        m = re.search(r"Used (\d+) registers", line)
+        if not m:
+            continue
+        for pattern, regs in REDISTRIBUTED:
+            if pattern.search(name):
+                seen += 1
+                if (int(m.group(1)) + 7) // 8 * 8 < regs:
+                    raise RuntimeError(f"{name} was compiled to {m.group(1)} registers, it hands out {regs}")
+        name = ""
+    return seen
+
+
+def _compile(src: str, extra, verbose: bool) -> str:
     obj = os.path.join(BUILD_DIR, os.path.basename(src) + ".o")
-    cmd = [NVCC, *ARCH, *FLAGS, *extra, "-c", src, "-o", obj]
-    subprocess.check_call(cmd)
+    cmd = [NVCC, *ARCH, *FLAGS, *extra, "-Xptxas", "-v", "-c", src, "-o", obj]
+    r = subprocess.run(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True)
+    if verbose or r.returncode or "warning" in r.stdout:
+        sys.stderr.write(r.stdout)
+    r.check_returncode()
+    check_registers(r.stdout)
     return obj
 
 
@@ -50,9 +81,8 @@ def build(force: bool = False, verbose: bool = False, extra=()) -> str:
     if not force and up_to_date():
         return OUT
     os.makedirs(BUILD_DIR, exist_ok=True)
-    extra = list(extra) + (["-Xptxas", "-v"] if verbose else [])
     with cf.ThreadPoolExecutor(max_workers=min(8, os.cpu_count() or 1)) as ex:
-        objs = list(ex.map(lambda s: _compile(s, extra), _sources()))
+        objs = list(ex.map(lambda s: _compile(s, extra, verbose), _sources()))
     tmp = OUT + ".tmp"
     subprocess.check_call([NVCC, *ARCH, "-shared", "-o", tmp, *objs, "-lcublas"])
     os.replace(tmp, OUT)

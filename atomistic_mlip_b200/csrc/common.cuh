@@ -70,10 +70,14 @@ inline cudaError_t launch_after(void (*k)(P...), dim3 grid, dim3 block, size_t s
 // that one wrote can be read.
 __device__ __forceinline__ void after_previous() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
+// A thread is launched with its kernel's registers rounded up to a multiple of eight.
+constexpr bool launch_regs_cover(int compiled, int wanted) { return (compiled + 7) / 8 * 8 >= wanted; }
+static_assert(launch_regs_cover(72, 72) && launch_regs_cover(65, 72) && launch_regs_cover(80, 72) && !launch_regs_cover(64, 72), "");
+
 // Dynamic shared memory of kernel K (always the same size), allowed once per
 // device: the attribute call costs as much host time as a quarter of a launch.
-// regs: registers a thread that K must have been compiled to (a kernel that
-// redistributes them with setmaxnreg would wait for ever with fewer).
+// regs: registers a thread that K needs at launch (a kernel that redistributes them
+// with setmaxnreg would wait for ever with fewer; the build checks them as well).
 template <auto K> cudaError_t allow_smem(size_t bytes, int regs = 0) {
   static std::atomic<uint64_t> done{0};
   int dev = 0;
@@ -85,7 +89,7 @@ template <auto K> cudaError_t allow_smem(size_t bytes, int regs = 0) {
     cudaFuncAttributes at;
     e = cudaFuncGetAttributes(&at, K);
     if (e != cudaSuccess) return e;
-    if (at.numRegs != regs) return cudaErrorInvalidDeviceFunction;
+    if (!launch_regs_cover(at.numRegs, regs)) return cudaErrorInvalidDeviceFunction;
   }
   e = cudaFuncSetAttribute(K, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
   if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_relaxed);
