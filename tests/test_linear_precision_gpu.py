@@ -1,0 +1,80 @@
+"""What the linear layers' kernels do for their precision, each at a size where its
+loss would show: three terms of an fp32 operand, and chains of MMAs that end.
+
+Three terms: an fp32 value times one, plus zeros, is itself.
+Chains: the tensor core's accumulation truncates, by measurement about 1e-8 of the
+sum per MMA of 16 products, all in one direction where the products have one sign.
+A chain ends after 1,024 products (64 MMAs: 6.4e-7; twice that is allowed), and the
+K / 1,024 pieces are added with a rounding each (2^-24).  One chain over 16,384
+products would be off by 1e-5, five times the bound."""
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+K = 16384
+CHAIN = 2 * 64 * 1e-8 + K / 1024 * 2.0 ** -24
+
+
+def _full_mantissas(r, c, g):
+    """Values whose 24 bits all matter, over some 40 powers of two."""
+    import torch
+    m = torch.randint(1 << 23, 1 << 24, (r, c), generator=g, device="cuda").float() + 0.0
+    m = m * torch.exp2(torch.randint(-43, -3, (r, c), generator=g, device="cuda").float())
+    return m * (torch.randint(0, 2, (r, c), generator=g, device="cuda") * 2 - 1)
+
+
+# short and split contractions, a chain of several pieces; rows that are and are not
+# whole 16-byte pieces
+@pytest.mark.parametrize("M,K,pad", [(600, 600, 0), (300, 1200, 0), (1600, 1160, 0), (1601, 1163, 0), (600, 515, 3)])
+def test_fp32_operands_keep_every_bit(cuda_ok, M, K, pad):
+    """Through permutations, from either operand of all three products."""
+    import torch
+    from atomistic_mlip_b200 import e2f
+    g = torch.Generator(device="cuda")
+    g.manual_seed(M + K)
+    wide = lambda t: torch.nn.functional.pad(t, (0, pad))[:, :t.shape[1]]
+    x, perm = _full_mantissas(M, K, g), torch.randperm(K, generator=g, device="cuda")
+    P = torch.eye(K, device="cuda")[perm]                       # P x = x[perm], x P^T = x[:, perm]
+    xw, Pw = wide(x), wide(P)
+    assert torch.equal(e2f.linear_forward(xw, Pw), x[:, perm])
+    assert torch.equal(e2f.linear_forward(Pw, xw), x[:, perm].t())
+    dy = _full_mantissas(M, K, g)
+    gx, _, _ = e2f.linear_backward(torch.zeros(M, K, device="cuda"), Pw, dy, need_W=False)   # dy P
+    assert torch.equal(gx, dy[:, torch.argsort(perm)])
+    W = _full_mantissas(K, M, g)
+    gx, _, _ = e2f.linear_backward(torch.zeros(K, M, device="cuda"), wide(W), P, need_W=False)   # P W
+    assert torch.equal(gx, W[perm])
+    _, gw, _ = e2f.linear_backward(wide(W), torch.zeros(K, M, device="cuda"), P, need_x=False)   # P^T W
+    assert torch.equal(gw, W[torch.argsort(perm)])
+    D = _full_mantissas(K, M, g)
+    _, gw, _ = e2f.linear_backward(Pw, torch.zeros(M, K, device="cuda"), D, need_x=False)        # D^T P
+    assert torch.equal(gw, D.t()[:, torch.argsort(perm)])
+    assert e2f.stream_status() == 0
+
+
+@pytest.mark.parametrize("dt", ["float32", "bfloat16"])
+def test_long_sums_of_one_sign(cuda_ok, dt):
+    """144 tiles: contractions that are not split, so that only the ends of the chains
+    keep the error down."""
+    import torch
+    from atomistic_mlip_b200 import e2f
+    M = 1536
+    g = torch.Generator(device="cuda")
+    g.manual_seed(5)
+    dt = getattr(torch, dt)
+    x = (torch.rand(M, K, generator=g, device="cuda") * 0.5 + 0.5).to(dt)
+    W = (torch.rand(M, K, generator=g, device="cuda") * 0.5 + 0.5).to(dt)
+    want = x.double() @ W.double().t()
+    out = e2f.linear_forward(x, W, out_dtype=torch.float32)
+    assert float(((out.double() - want) / want).abs().max()) <= CHAIN
+    r = torch.rand(M, M, generator=g, device="cuda")
+    out = e2f.linear_forward(x, W, bias=r[0].contiguous(), residual=r, out_dtype=torch.float32)
+    full = want + r[0].double() + r.double()
+    assert float(((out.double() - full) / full).abs().max()) <= CHAIN + 2.0 ** -23
+    if dt == torch.float32:
+        a, b = x.t().contiguous(), W.t().contiguous()          # [K, M]
+        _, gw, _ = e2f.linear_backward(b, torch.zeros(M, M, device="cuda"), a, need_x=False)   # a^T b
+        assert float(((gw.double() - want) / want).abs().max()) <= CHAIN
+        gx, _, _ = e2f.linear_backward(torch.zeros(M, M, device="cuda"), b, x, need_W=False)   # x b
+        assert float(((gx.double() - want) / want).abs().max()) <= CHAIN
+    assert e2f.stream_status() == 0
