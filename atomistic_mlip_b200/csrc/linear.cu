@@ -9,7 +9,8 @@
 // with one or two rows or outputs (linear_skinny.cu), up to 16 inputs
 // (linear_thin.cu) or too few tiles to fill them (linear_small.cu).  bf16 operands are used as they are, fp32
 // accumulation.  fp32 operands are split into three bf16 terms each,
-// x = h + m + l (8 + 8 + 8 significant bits: exact), and the products
+// x = h + m + l (8 + 8 + 8 significant bits: exact, down to the least bf16 value,
+// which leaves 2^-133 of operands below 2^-109), and the products
 // h h', (h m' + m h' + h l' + l h' + m m') are summed in two accumulators; the
 // terms left out are below 2^-24 of a product, so the result is that of an
 // fp32 product at six bf16 products' cost (nominal 375 TFLOP/s against 74 on

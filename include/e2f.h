@@ -374,7 +374,8 @@ typedef struct e2f_linear {
   int64_t M;           /* rows, 0 .. E2F_MAX_ROWS */
   int32_t K, N;        /* inputs and outputs, 1 .. 2^20 */
   const void *x;       /* device [M][K], row m at x + m ldx */
-  int64_t ldx;         /* elements from row to row, >= K: Q C reads the l = 0 rows of [M][Q][C] in place */
+  int64_t ldx;         /* elements from row to row, >= K: Q C reads the l = 0 rows of [M][Q][C] in place.
+                          Every row stride of these calls is at most 2^29 (E2F_ERR_INVALID_ARG) */
   const void *W;       /* device [N][K] (out x in), row n at W + n ldw */
   int64_t ldw;         /* >= K */
   const float *bias;   /* device fp32 [N], or NULL */
@@ -389,7 +390,9 @@ typedef struct e2f_linear {
  *             for either dtype); elements between the rows are left alone.
  * bf16 products are accumulated in fp32; E2F_F32 products are as accurate
  * as fp32 multiply-adds (which small ones are; the others take three bf16 terms
- * per operand on the tensor cores).  The sum, bias, activation and residual are
+ * per operand on the tensor cores, which hold an operand to 2^-133: where one is
+ * below 2^-109 in magnitude that is less than its 24 bits, and beside an infinity
+ * one of 2^-133 or less may count as zero).  The sum, bias, activation and residual are
  * formed in fp32 and rounded once.
  * Pointers need only their element's alignment, strides any value (16-byte
  * aligned pointers and rows run fastest).  out may overlap no input but the

@@ -83,6 +83,31 @@ def test_values_beyond_the_bf16_range(cuda_ok, M, K):
     assert e2f.stream_status() == 0
 
 
+@pytest.mark.parametrize("M,K", [(600, 512), (1600, 1200)])
+def test_fp32_operands_of_small_magnitude(cuda_ok, M, K):
+    """Operands are held to 2^-133: from 2^-109 on that is half of their last bit, and
+    below it the error stays there, whatever the other operand.  By arithmetic: half
+    of the operand is rounded to fp32 (whose least step is 2^-149: off by 2^-150, so
+    by 2^-149 of the operand), its terms to bf16 (least step 2^-133: off by 2^-134, so
+    by 2^-133); results are rounded to fp32 (2^-24, or 2^-150 where they are below its
+    normal range, times four after the halving)."""
+    import torch
+    from atomistic_mlip_b200 import e2f
+    g = torch.Generator(device="cuda")
+    g.manual_seed(M)
+    for w in (1.0, 2.0 ** 60, 2.0 ** 100):
+        eye = torch.eye(K, device="cuda") * w
+        for e in (-90, -108, -112, -120, -126, -130, -140, -149):
+            x = (torch.rand(M, K, generator=g, device="cuda", dtype=torch.float64) + 1).mul(2.0 ** e).float()
+            want = x.double() * w
+            tol = (2.0 ** -133 + 2.0 ** -149) * w + 2.0 ** -24 * want.abs() + 2.0 ** -148
+            assert bool(((e2f.linear_forward(x, eye).double() - want).abs() <= tol).all())
+            assert bool(((e2f.linear_forward(eye, x).double() - want.t()).abs() <= tol.t()).all())
+            if e >= -108:
+                assert torch.equal(e2f.linear_forward(x, eye).double(), want.float().double())
+    assert e2f.stream_status() == 0
+
+
 def test_nan_costs_nothing(cuda_ok):
     """A diverged step takes no longer than another one (medians of device times; the
     factor of three leaves room for a clock that changes between them)."""
