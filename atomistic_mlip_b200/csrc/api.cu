@@ -32,12 +32,34 @@ struct DeviceState {
 static std::mutex g_mu;
 static DeviceState g_dev[MAX_DEVICES];
 
+// While it lives, this thread may allocate although a stream is being captured (what
+// it allocates is not part of the captured work).
+struct OutsideCapture {
+  cudaStreamCaptureMode mode = cudaStreamCaptureModeRelaxed;
+  OutsideCapture() { cudaThreadExchangeStreamCaptureMode(&mode); }
+  ~OutsideCapture() { cudaThreadExchangeStreamCaptureMode(&mode); }
+};
+
+// An int of zero on the current device.
+static int *new_flag() {
+  int *p = nullptr;
+  cudaStream_t s = nullptr;   // (the default stream may wait for a captured one)
+  bool ok = cudaMalloc(&p, sizeof(int)) == cudaSuccess;
+  ok = ok && cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking) == cudaSuccess;
+  ok = ok && cudaMemsetAsync(p, 0, sizeof(int), s) == cudaSuccess && cudaStreamSynchronize(s) == cudaSuccess;
+  if (s) cudaStreamDestroy(s);
+  if (!ok && p) cudaFree(p);
+  return ok ? p : nullptr;
+}
+
 static DeviceState *device_state() {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return nullptr;
   if (dev < 0 || dev >= MAX_DEVICES) return nullptr;
   std::lock_guard<std::mutex> lk(g_mu);
   DeviceState &d = g_dev[dev];
+  if (d.pool && d.err_flag) return &d;
+  const OutsideCapture relaxed;   // the first call may be a captured one
   if (!d.pool) {
     cudaMemPoolProps props;
     memset(&props, 0, sizeof(props));
@@ -49,11 +71,8 @@ static DeviceState *device_state() {
     uint64_t thr = UINT64_MAX;   // keep freed blocks for reuse by later calls
     cudaMemPoolSetAttribute(d.pool, cudaMemPoolAttrReleaseThreshold, &thr);
   }
-  if (!d.err_flag) {
-    if (cudaMalloc(&d.err_flag, sizeof(int)) != cudaSuccess) { d.err_flag = nullptr; return nullptr; }
-    if (cudaMemset(d.err_flag, 0, sizeof(int)) != cudaSuccess) return nullptr;
-  }
-  return &d;
+  if (!d.err_flag) d.err_flag = new_flag();
+  return d.err_flag ? &d : nullptr;
 }
 
 cudaError_t pool_alloc(void **p, size_t bytes, cudaStream_t s) {
