@@ -9,6 +9,8 @@ K / 1,024 pieces are added with a rounding each (2^-24).  One chain over 16,384
 products would be off by 1e-5, five times the bound."""
 import pytest
 
+from .test_linear_gpu import _check_backward, _check_forward, _make
+
 pytestmark = pytest.mark.gpu
 
 K = 16384
@@ -77,4 +79,23 @@ def test_long_sums_of_one_sign(cuda_ok, dt):
         assert float(((gw.double() - want) / want).abs().max()) <= CHAIN
         gx, _, _ = e2f.linear_backward(torch.zeros(M, M, device="cuda"), b, x, need_W=False)   # x b
         assert float(((gx.double() - want) / want).abs().max()) <= CHAIN
+    assert e2f.stream_status() == 0
+
+
+@pytest.mark.parametrize("M,C,N", [(10513, 1427, 9), (9473, 1025, 40), (18945, 1088, 3), (6000, 2051, 130), (200, 4099, 300)])
+@pytest.mark.parametrize("dt", ["float32", "bfloat16"])
+def test_split_contractions_of_tall_products(cuda_ok, M, C, N, dt):
+    """Tiles that leave a wave of SMs uneven, so that contractions through registers
+    are split into several parts (rows off 16-byte boundaries for bf16), forward, in
+    place on the residual, and backward."""
+    import torch
+    from atomistic_mlip_b200 import e2f
+    x, W, b, g = _make(M, C + 1, N, 1, getattr(torch, dt), M + N)
+    x, W = x[:, 1:], W[:, 1:]
+    r = torch.randn(M, N, generator=g, device="cuda")
+    _check_forward(e2f.linear_forward(x, W, bias=b, act="silu", out_dtype=torch.float32), x, W, b, None, "silu")
+    out = r.clone()
+    e2f.linear_forward(x, W, bias=b, residual=out, out=out, act="gelu")
+    _check_forward(out, x, W, b, r, "gelu")
+    _check_backward(*e2f.linear_backward(x, W, r, bias=b, act="silu"), x, W, b, r, "silu")
     assert e2f.stream_status() == 0
