@@ -42,8 +42,8 @@ bool small_fit(int M, int N, int K, int dtype, bool tma, bool extra);
 bool small_grads_fit(int M, int N, int K, int dtype);
 template <typename T> e2f_status gemm_small(const Gemm &g, cudaStream_t s);
 template <typename T>
-e2f_status small_grads(const e2f_linear &p, const void *dz, long long ldz, void *gx, long long ldgx, void *gW, long long ldgw,
-                       const void *cp, int ctype, long long cld, int crows, float *gb, bool after, cudaStream_t s);
+e2f_status small_grads(const e2f_linear &p, const void *dz, const void *dz2, long long ldz, void *gx, long long ldgx, void *gW,
+                       long long ldgw, const void *cp, int ctype, long long cld, int crows, float *gb, bool after, cudaStream_t s);
 
 constexpr int BM = 128, BN = 128, BK = 64, NT = 256;
 constexpr double ALIGN_WORK = 1 << 29;   // multiply-adds from which unaligned operands are copied first
@@ -327,13 +327,18 @@ static e2f_status backward(const e2f_linear &arg, const void *dy, int64_t ldg, i
   const bool own = p.act != E2F_ACT_NONE || out_dtype != TT;
   const long long lddz = (N + 7) & ~7;
   auto up = [](size_t b) { return (b + 255) & ~(size_t)255; };
-  const size_t zb = own && prod ? up(sizeof(T) * (size_t)M * lddz) : 0;
+  // (bf16: two terms, 16 bits of it.  With one, rounding dz added as much error to
+  // grad_x and grad_W as rounding them: 2.35e-3 of their norm instead of 1.66e-3, for
+  // which the second one costs 100,002 x 128 -> 512 125 -> 175 us, 4,099 x 1,000 ->
+  // 2,050 107 -> 137.)
+  const bool two = TT == E2F_BF16;
+  const size_t zp = own && prod ? up(sizeof(T) * (size_t)M * lddz) : 0, zb = two ? 2 * zp : zp;
   // partial rows of the column sums, and two buffers for the sums of 1,024 rows each
   const int64_t cr = own ? colpart_rows(M) : 0, cr2 = (std::max<int64_t>(cr, M) + CROWS - 1) / CROWS;
   const size_t cb = gb ? sizeof(float) * (size_t)(cr + 2 * cr2) * N : 0;
   Scratch ws;
   if (zb + cb) E2F_CUDA_TRY(ws.alloc(zb + cb, s));
-  const void *dz = dy;
+  const void *dz = dy, *dz2 = nullptr;
   long long ldz = ldg;
   // what the column sums are taken of
   const void *cp = dy;
@@ -346,7 +351,7 @@ static e2f_status backward(const e2f_linear &arg, const void *dy, int64_t ldg, i
     g.M = M; g.N = N; g.K = K;
     g.e.mode = MODE_DZ; g.e.act = p.act; g.e.bias = p.bias;
     g.e.extra = dy; g.e.lde = ldg; g.e.etype = out_dtype;
-    g.e.out = prod ? ws.p : nullptr; g.e.ldo = lddz; g.e.otype = TT;
+    g.e.out = prod ? ws.p : nullptr; g.e.out2 = prod && two ? ws.as<char>() + zp : nullptr; g.e.ldo = lddz; g.e.otype = TT;
     g.e.colpart = gb ? reinterpret_cast<float *>(ws.as<char>() + zb) : nullptr;
     crows = (int)((M + FROWS - 1) / FROWS);
     if (p.act != E2F_ACT_NONE) {
@@ -358,11 +363,11 @@ static e2f_status backward(const e2f_linear &arg, const void *dy, int64_t ldg, i
       E2F_LIN_LAUNCH(g, finish_kernel, grid, NT, 0, s, (const float *)nullptr, 0, M, N, g.e);
     }
     after = true;
-    if (prod) { dz = ws.p; ldz = lddz; }
+    if (prod) { dz = ws.p; dz2 = g.e.out2; ldz = lddz; }
     cp = g.e.colpart; ctype = E2F_F32; cld = N;
   }
   if (small_grads_fit(M, N, K, TT))
-    return small_grads<T>(p, dz, ldz, gx, ldgx, gW, ldgw, cp, ctype, cld, crows, gb, after, s);
+    return small_grads<T>(p, dz, dz2, ldz, gx, ldgx, gW, ldgw, cp, ctype, cld, crows, gb, after, s);
   if (gb) {
     float *to = reinterpret_cast<float *>(ws.as<char>() + zb) + (size_t)cr * N, *other = to + (size_t)cr2 * N;
     for (;;) {
@@ -378,7 +383,7 @@ static e2f_status backward(const e2f_linear &arg, const void *dy, int64_t ldg, i
   }
   if (gx) {
     Gemm g{};
-    g.A = dz; g.lda = ldz; g.B = p.W; g.ldb = p.ldw;
+    g.A = dz; g.A2 = dz2; g.lda = ldz; g.B = p.W; g.ldb = p.ldw;
     g.M = M; g.N = K; g.K = N;
     g.after = after;
     after = true;
@@ -389,7 +394,7 @@ static e2f_status backward(const e2f_linear &arg, const void *dy, int64_t ldg, i
   }
   if (gW) {
     Gemm g{};
-    g.A = dz; g.lda = ldz; g.B = p.x; g.ldb = p.ldx;
+    g.A = dz; g.A2 = dz2; g.lda = ldz; g.B = p.x; g.ldb = p.ldx;
     g.M = N; g.N = K; g.K = M;
     g.after = after;
     g.e.mode = MODE_OUT; g.e.act = E2F_ACT_NONE;

@@ -27,6 +27,7 @@ struct Epi {
   long long lde;
   int etype;
   void *out;
+  void *out2;       // MODE_DZ, bf16: what out leaves of the value, in bf16 and out's layout, or absent
   long long ldo;
   int otype;
   float *colpart;   // MODE_DZ: column sums of out per row block, fp32 [row blocks][N], or absent
@@ -36,6 +37,7 @@ struct Epi {
 // A(m, k) = A[k lda + m]; the same for B.
 struct Gemm {
   const void *A, *B;
+  const void *A2;    // bf16: a second term of A in the same layout (A + A2 is meant), or absent
   long long lda, ldb;
   int M, N, K;
   int kper;          // contraction blocks (of BK) per split
@@ -162,6 +164,23 @@ __device__ __forceinline__ f2 gelu_grad(f2 z) {
   return fma2(mul2(z, both(0.39894228f)), e, p);
 }
 
+// Two bf16 terms of each of a pair, together 16 bits: h the nearest, l what it leaves
+// (nothing where h is not finite).
+__device__ __forceinline__ void two_terms(f2 v, uint32_t &h, uint32_t &l) {
+  h = pack_bf16x2(v.x, v.y);
+  const f2 r = fma2({__uint_as_float(h << 16), __uint_as_float(h & 0xffff0000u)}, both(-1.f), v);
+  l = pack_bf16x2(fabsf(r.x) < INFINITY ? r.x : 0.f, fabsf(r.y) < INFINITY ? r.y : 0.f);
+}
+// The same of one value that may meet infinities in a product (dz = dL/dout, without
+// an activation whose derivative would be NaN beside them): h is cut, not rounded, so
+// that l has its sign, and l is zero only where h is: infinity times either of them
+// is the same infinity.
+__device__ __forceinline__ void two_terms(float v, __nv_bfloat16 &h, __nv_bfloat16 &l) {
+  h = __float2bfloat16_rz(v);
+  const float w = __bfloat162float(h);
+  l = __float2bfloat16_rn(copysignf(fmaxf(fabsf(v - w), fabsf(w) * 0x1p-30f), v));
+}
+
 __device__ __forceinline__ float act_fwd(int act, float z) {
   return act == E2F_ACT_SILU ? silu(z) : act == E2F_ACT_GELU ? gelu(z) : z;
 }
@@ -189,7 +208,11 @@ __device__ __forceinline__ float epi_elem(const Epi &e, long long m, int n, floa
     return 0.f;
   }
   v = __fmul_rn(act_bwd(e.act, v), load_as(e.extra, e.etype, (size_t)(m * e.lde) + n));
-  if (e.out) store_as(e.out, e.otype, (size_t)(m * e.ldo) + n, v);
+  if (e.out) {
+    const size_t i = (size_t)(m * e.ldo) + n;
+    if (e.out2) two_terms(v, static_cast<__nv_bfloat16 *>(e.out)[i], static_cast<__nv_bfloat16 *>(e.out2)[i]);
+    else store_as(e.out, e.otype, i, v);
+  }
   return v;
 }
 

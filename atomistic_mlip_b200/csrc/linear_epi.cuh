@@ -97,6 +97,7 @@ struct Rows {
   char *out;                     // row m0 + lane / 4 of the results (or partial sums)
   const char *extra;
   long long ostep, xstep;        // eight rows on
+  long long rest;                // from out to out2, 0 if there is none
 };
 __device__ __forceinline__ Rows rows_of(const Gemm &g, int split, int m0, int lane) {
   Rows r;
@@ -111,6 +112,7 @@ __device__ __forceinline__ Rows rows_of(const Gemm &g, int split, int m0, int la
     r.out = static_cast<char *>(g.e.out) + (size_t)(m * g.e.ldo) * sz;
     r.ostep = 8 * g.e.ldo * sz;
   }
+  r.rest = g.e.out2 ? static_cast<char *>(g.e.out2) - static_cast<char *>(g.e.out) : 0;
   const int xz = g.e.etype == E2F_F32 ? 4 : 2;
   r.extra = static_cast<const char *>(g.e.extra) + (size_t)(m * g.e.lde) * xz;
   r.xstep = 8 * g.e.lde * xz;
@@ -187,7 +189,19 @@ __device__ __forceinline__ void put_rows(const Rows &rw, const Extra &x, const f
         if (EPI == DZ) cs[j] = add2(cs[j], r[j]);
       }
     }
-    if (store) store8<OT>(o, r);
+    if (EPI == DZ && sizeof(OT) == 2) {
+      if (store) {
+        uint4 h, l;
+        two_terms(r[0], h.x, l.x);
+        two_terms(r[1], h.y, l.y);
+        two_terms(r[2], h.z, l.z);
+        two_terms(r[3], h.w, l.w);
+        *reinterpret_cast<uint4 *>(o) = h;
+        *reinterpret_cast<uint4 *>(o + rw.rest) = l;
+      }
+    } else if (store) {
+      store8<OT>(o, r);
+    }
   }
 }
 
@@ -310,7 +324,7 @@ __device__ __forceinline__ void epi_chunk(const Gemm &g, int vec, int split, con
             w = EPI == RES ? w + y : __fmul_rn(w, y);
             sum += w;
           }
-          if (store) {
+          if (store) {   // (UA: fp32 operands, so without a second term)
             if (of) *reinterpret_cast<float *>(o) = w;
             else *reinterpret_cast<__nv_bfloat16 *>(o) = __float2bfloat16_rn(w);
           }
@@ -338,7 +352,12 @@ __device__ __forceinline__ void epi_chunk(const Gemm &g, int vec, int split, con
             w = EPI == RES ? w + y[r] : __fmul_rn(w, y[r]);
             sum += w;
           }
-          if (EPI != DZ || e.out) store_as(e.out, e.otype, (size_t)(m * e.ldo) + nl, w);
+          const size_t i = (size_t)(m * e.ldo) + nl;
+          if (EPI == DZ && e.out2) {
+            two_terms(w, static_cast<__nv_bfloat16 *>(e.out)[i], static_cast<__nv_bfloat16 *>(e.out2)[i]);
+          } else if (EPI != DZ || e.out) {
+            store_as(e.out, e.otype, i, w);
+          }
         }
       }
     }

@@ -26,9 +26,11 @@ constexpr int CONV = 512, CTRL_WARP = 16, EPI_WARP = 20, NT = 896, LAUNCH_REGS =
 constexpr int TILE_BYTES = 128 * BK * 2;     // one 128 x 64 bf16 operand tile
 template <typename T> constexpr int terms() { return sizeof(T) == 4 ? 3 : 1; }
 template <typename T> constexpr int stages() { return sizeof(T) == 4 ? 2 : 4; }
-template <typename T> constexpr int ring() { return stages<T>() * 2 * terms<T>() * TILE_BYTES; }
+// NA: terms of A in memory, each bf16, multiplied with B one after the other (dz of
+// the bf16 backward; 1 for all else)
+template <typename T, int NA> constexpr int ring() { return stages<T>() * (NA + 1) * terms<T>() * TILE_BYTES; }
 constexpr int STAGING = 8 * 32 * 32 * 4, SBIAS = 8 * 32 * 4;
-template <typename T> constexpr size_t smem_bytes() { return ring<T>() + STAGING + SBIAS + 256 + 1024; }
+template <typename T, int NA> constexpr size_t smem_bytes() { return ring<T, NA>() + STAGING + SBIAS + 256 + 1024; }
 
 struct Args {
   Gemm g;
@@ -148,10 +150,11 @@ template <typename T, bool MN> __device__ __forceinline__ void put_tile(const Ra
 
 // Registers: 16 carrying warps 64, four control warps 24, eight epilogue warps
 // 112 of the 72 a thread the block is launched with: 4 * 64 + 24 + 2 * 112 = 7 * 72.
-template <typename T, bool AMN, bool BMN, int EPI, bool LONGK>
+template <typename T, bool AMN, bool BMN, int EPI, bool LONGK, int NA>
 __global__ void __launch_bounds__(NT, 1) gemm_reg_kernel(const __grid_constant__ Args a) {
   using namespace tc;
-  constexpr int NS = terms<T>(), ST = stages<T>(), OP = NS * TILE_BYTES, RING = ring<T>();
+  constexpr int NS = terms<T>(), ST = stages<T>(), OP = NS * TILE_BYTES, RING = ring<T, NA>();
+  constexpr int OA = NA * OP, SB = OA + OP;   // A's part of a stage, the stage
   constexpr int ACC = NS == 3 ? 256 : 128;   // TMEM columns of an accumulator
   constexpr uint32_t LIMIT = 1u << 26;
   extern __shared__ uint8_t smem_raw[];
@@ -178,10 +181,10 @@ __global__ void __launch_bounds__(NT, 1) gemm_reg_kernel(const __grid_constant__
 
   if (warp < CTRL_WARP) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 64;");
-    const T *A = static_cast<const T *>(g.A), *B = static_cast<const T *>(g.B);
-    const bool va = ((reinterpret_cast<uintptr_t>(A) | (uintptr_t)(g.lda * sizeof(T))) & 15) == 0;
+    const T *A = static_cast<const T *>(g.A), *A2 = static_cast<const T *>(g.A2), *B = static_cast<const T *>(g.B);
+    const bool va = ((reinterpret_cast<uintptr_t>(A) | reinterpret_cast<uintptr_t>(A2) | (uintptr_t)(g.lda * sizeof(T))) & 15) == 0;
     const bool vb = ((reinterpret_cast<uintptr_t>(B) | (uintptr_t)(g.ldb * sizeof(T))) & 15) == 0;
-    Raw<T> ra[2], rb[2];
+    Raw<T> ra[2], ra2[2], rb[2];
     int i = blockIdx.x, s = 0;
     uint32_t ph = 1;   // the first pass over the ring finds it empty
     bool ok = true;
@@ -189,13 +192,15 @@ __global__ void __launch_bounds__(NT, 1) gemm_reg_kernel(const __grid_constant__
       Tile t = tile_of(g, a.s, i);
       int kb = t.kb0;
       fetch_tile<T, AMN>(ra, A, g.lda, t.m0, g.M, kb * BK, g.K, va);
+      if (NA == 2) fetch_tile<T, AMN>(ra2, A2, g.lda, t.m0, g.M, kb * BK, g.K, va);
       fetch_tile<T, BMN>(rb, B, g.ldb, t.n0, min(g.N, t.n0 + a.s.bn), kb * BK, g.K, vb);
       while (true) {
         ok = __all_sync(0xffffffffu, mbar_wait(&empty[s], ph, LIMIT));
         if (!ok) break;
-        uint8_t *sA = smem + s * 2 * OP;
+        uint8_t *sA = smem + s * SB;
         put_tile<T, AMN>(ra, sA, BM);
-        put_tile<T, BMN>(rb, sA + OP, min(a.s.bn, (g.N - t.n0 + 15) & ~15));
+        if (NA == 2) put_tile<T, AMN>(ra2, sA + OP, BM);
+        put_tile<T, BMN>(rb, sA + OA, min(a.s.bn, (g.N - t.n0 + 15) & ~15));
         fence_async_smem();
         __syncwarp();
         if (lane == 0) mbar_arrive(&full[s]);
@@ -207,6 +212,7 @@ __global__ void __launch_bounds__(NT, 1) gemm_reg_kernel(const __grid_constant__
           kb = t.kb0;
         }
         fetch_tile<T, AMN>(ra, A, g.lda, t.m0, g.M, kb * BK, g.K, va);
+        if (NA == 2) fetch_tile<T, AMN>(ra2, A2, g.lda, t.m0, g.M, kb * BK, g.K, va);
         fetch_tile<T, BMN>(rb, B, g.ldb, t.n0, min(g.N, t.n0 + a.s.bn), kb * BK, g.K, vb);
       }
     }
@@ -230,11 +236,12 @@ __global__ void __launch_bounds__(NT, 1) gemm_reg_kernel(const __grid_constant__
             ok = mbar_wait(&full[s], ph, LIMIT);
             if (!ok) break;
             tc_fence_after();
-            const uint32_t a0 = smem_addr(smem + s * 2 * OP), b0 = a0 + OP;
+            const uint32_t a0 = smem_addr(smem + s * SB), b0 = a0 + OA;
 #pragma unroll
             for (int k = 0; k < BK; k += 16) {
               const uint32_t more = kb > kc || k > 0 ? 1u : 0u;
               mma_bf16_ss(acc, tile_desc<AMN>(a0, k), tile_desc<BMN>(b0, k), id, more);
+              if (NA == 2) mma_bf16_ss(acc, tile_desc<AMN>(a0 + OP, k), tile_desc<BMN>(b0, k), id, 1u);
               if (NS == 3) {
                 const uint32_t am = a0 + TILE_BYTES, al = am + TILE_BYTES, bm = b0 + TILE_BYTES, bl = bm + TILE_BYTES;
                 mma_bf16_ss(acc + 128, tile_desc<AMN>(a0, k), tile_desc<BMN>(bl, k), id, more);
@@ -361,16 +368,17 @@ __global__ void __launch_bounds__(NT, 1) gemm_reg_kernel(const __grid_constant__
   if (warp == CTRL_WARP) tmem_dealloc(tmem, 2 * ACC);
 }
 
-template <typename T, bool AMN, bool BMN, int EPI>
+template <typename T, bool AMN, bool BMN, int EPI, int NA = 1>
 static e2f_status launch(const Args &a, int sms, cudaStream_t s) {
+  constexpr size_t smem = smem_bytes<T, NA>();
   if (long_chain(a.g)) {
-    constexpr auto k = gemm_reg_kernel<T, AMN, BMN, EPI, true>;
-    E2F_CUDA_TRY(allow_smem<k>(smem_bytes<T>(), LAUNCH_REGS));
-    E2F_LIN_LAUNCH(a.g, k, std::min(a.s.tiles, sms), NT, smem_bytes<T>(), s, a);
+    constexpr auto k = gemm_reg_kernel<T, AMN, BMN, EPI, true, NA>;
+    E2F_CUDA_TRY(allow_smem<k>(smem, LAUNCH_REGS));
+    E2F_LIN_LAUNCH(a.g, k, std::min(a.s.tiles, sms), NT, smem, s, a);
   } else {
-    constexpr auto k = gemm_reg_kernel<T, AMN, BMN, EPI, false>;
-    E2F_CUDA_TRY(allow_smem<k>(smem_bytes<T>(), LAUNCH_REGS));
-    E2F_LIN_LAUNCH(a.g, k, std::min(a.s.tiles, sms), NT, smem_bytes<T>(), s, a);
+    constexpr auto k = gemm_reg_kernel<T, AMN, BMN, EPI, false, NA>;
+    E2F_CUDA_TRY(allow_smem<k>(smem, LAUNCH_REGS));
+    E2F_LIN_LAUNCH(a.g, k, std::min(a.s.tiles, sms), NT, smem, s, a);
   }
   return E2F_OK;
 }
@@ -395,6 +403,8 @@ e2f_status gemm_reg(const Gemm &g, int splits, int bn, int sms, cudaStream_t s) 
       default: break;
     }
   }
+  if constexpr (BMN && sizeof(T) == 2)   // the products of dz
+    if (g.A2) return launch<T, AMN, BMN, PLAIN, 2>(a, sms, s);
   return launch<T, AMN, BMN, PLAIN>(a, sms, s);
 }
 template e2f_status gemm_reg<float, false, false>(const Gemm &, int, int, int, cudaStream_t);

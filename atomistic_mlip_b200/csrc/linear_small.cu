@@ -15,15 +15,22 @@ namespace small {
 
 constexpr int NT = 256, TS = 32, PITCH = TS + 2;
 
+// The value that two terms stand for (see two_terms: beside an infinite one the second
+// adds nothing).
+__device__ __forceinline__ float terms_sum(float h, float l) { return fabsf(h) < INFINITY ? h + l : h; }
+
 // Four elements of a 32 x 32 operand piece (row r of r0 .., contraction k of
 // k0 ..) a thread; CONTIG: the contraction index is the contiguous one.
+// P2: a second term of every element, or null.
 template <typename T, bool CONTIG>
-__device__ __forceinline__ void fetch(float (&v)[4], const T *P, long long ld, int r0, int rn, int k0, int kn) {
+__device__ __forceinline__ void fetch(float (&v)[4], const T *P, const T *P2, long long ld, int r0, int rn, int k0, int kn) {
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
     const int f = threadIdx.x & 31, s = (threadIdx.x >> 5) + 8 * j;
     const int r = r0 + (CONTIG ? s : f), k = k0 + (CONTIG ? f : s);
-    v[j] = r < rn && k < kn ? to_f(P[CONTIG ? (size_t)(r * ld) + k : (size_t)(k * ld) + r]) : 0.f;
+    const size_t i = CONTIG ? (size_t)(r * ld) + k : (size_t)(k * ld) + r;
+    v[j] = r < rn && k < kn ? to_f(P[i]) : 0.f;
+    if (P2 && r < rn && k < kn) v[j] = terms_sum(v[j], to_f(P2[i]));
   }
 }
 template <bool CONTIG> __device__ __forceinline__ void put(const float (&v)[4], float (*s)[PITCH]) {
@@ -36,21 +43,21 @@ template <bool CONTIG> __device__ __forceinline__ void put(const float (&v)[4], 
 
 // acc[i][j] = sum_k A(r, k) B(c, k) for r = r0 + 2 (t / 16) + i, c = c0 + 2 (t % 16) + j.
 template <typename T, bool A_CONTIG, bool B_CONTIG>
-__device__ __forceinline__ void product(float (&acc)[2][2], const T *A, long long lda, const T *B, long long ldb, int r0,
-                                        int rn, int c0, int cn, int kn, float (*sa)[PITCH], float (*sb)[PITCH]) {
+__device__ __forceinline__ void product(float (&acc)[2][2], const T *A, const T *A2, long long lda, const T *B, long long ldb,
+                                        int r0, int rn, int c0, int cn, int kn, float (*sa)[PITCH], float (*sb)[PITCH]) {
   const int ty = threadIdx.x >> 4, tx = threadIdx.x & 15;
   float va[4], vb[4];
   acc[0][0] = acc[0][1] = acc[1][0] = acc[1][1] = 0.f;
-  fetch<T, A_CONTIG>(va, A, lda, r0, rn, 0, kn);
-  fetch<T, B_CONTIG>(vb, B, ldb, c0, cn, 0, kn);
+  fetch<T, A_CONTIG>(va, A, A2, lda, r0, rn, 0, kn);
+  fetch<T, B_CONTIG>(vb, B, static_cast<const T *>(nullptr), ldb, c0, cn, 0, kn);
   for (int k0 = 0; k0 < kn; k0 += TS) {
     __syncthreads();
     put<A_CONTIG>(va, sa);
     put<B_CONTIG>(vb, sb);
     __syncthreads();
     if (k0 + TS < kn) {
-      fetch<T, A_CONTIG>(va, A, lda, r0, rn, k0 + TS, kn);
-      fetch<T, B_CONTIG>(vb, B, ldb, c0, cn, k0 + TS, kn);
+      fetch<T, A_CONTIG>(va, A, A2, lda, r0, rn, k0 + TS, kn);
+      fetch<T, B_CONTIG>(vb, B, static_cast<const T *>(nullptr), ldb, c0, cn, k0 + TS, kn);
     }
 #pragma unroll
     for (int k = 0; k < TS; ++k) {
@@ -63,10 +70,10 @@ __device__ __forceinline__ void product(float (&acc)[2][2], const T *A, long lon
   }
 }
 template <typename T, bool A_CONTIG>
-__device__ __forceinline__ void piece(const T *A, long long lda, const T *B, long long ldb, T *out, long long ldo, int r0,
+__device__ __forceinline__ void piece(const T *A, const T *A2, long long lda, const T *B, long long ldb, T *out, long long ldo, int r0,
                                       int rn, int c0, int cn, int kn, float (*sa)[PITCH], float (*sb)[PITCH]) {
   float acc[2][2];
-  product<T, A_CONTIG, false>(acc, A, lda, B, ldb, r0, rn, c0, cn, kn, sa, sb);
+  product<T, A_CONTIG, false>(acc, A, A2, lda, B, ldb, r0, rn, c0, cn, kn, sa, sb);
 #pragma unroll
   for (int i = 0; i < 2; ++i)
 #pragma unroll
@@ -81,8 +88,8 @@ template <typename T> __global__ void __launch_bounds__(NT) small_kernel(const _
   after_previous();
   const int nt = (g.N + TS - 1) / TS, r0 = blockIdx.x / nt * TS, c0 = blockIdx.x % nt * TS;
   float acc[2][2];
-  product<T, true, true>(acc, static_cast<const T *>(g.A), g.lda, static_cast<const T *>(g.B), g.ldb, r0, g.M, c0, g.N, g.K,
-                         sa, sb);
+  product<T, true, true>(acc, static_cast<const T *>(g.A), nullptr, g.lda, static_cast<const T *>(g.B), g.ldb, r0, g.M, c0,
+                         g.N, g.K, sa, sb);
   // lane = column through shared memory: rows out in contiguous pieces
   __syncthreads();
 #pragma unroll
@@ -112,7 +119,7 @@ template <typename T> __global__ void __launch_bounds__(NT) small_kernel(const _
 }
 
 struct Args {
-  const void *dz, *x, *W;
+  const void *dz, *dz2, *x, *W;   // dz2: dz's second term, or null
   long long ldz, ldx, ldw;
   void *gx, *gW;
   long long ldgx, ldgw;
@@ -127,16 +134,16 @@ struct Args {
 template <typename T> __global__ void __launch_bounds__(NT) small_grads_kernel(const __grid_constant__ Args a) {
   __shared__ float sa[TS][PITCH], sb[TS][PITCH];
   after_previous();
-  const T *dz = static_cast<const T *>(a.dz), *x = static_cast<const T *>(a.x), *W = static_cast<const T *>(a.W);
+  const T *dz = static_cast<const T *>(a.dz), *dz2 = static_cast<const T *>(a.dz2), *x = static_cast<const T *>(a.x), *W = static_cast<const T *>(a.W);
   const int kt = (a.K + TS - 1) / TS;
   int b = blockIdx.x;
   if (b < a.nx) {
-    piece<T, true>(dz, a.ldz, W, a.ldw, static_cast<T *>(a.gx), a.ldgx, b / kt * TS, a.M, b % kt * TS, a.K, a.N, sa, sb);
+    piece<T, true>(dz, dz2, a.ldz, W, a.ldw, static_cast<T *>(a.gx), a.ldgx, b / kt * TS, a.M, b % kt * TS, a.K, a.N, sa, sb);
     return;
   }
   b -= a.nx;
   if (b < a.nw) {
-    piece<T, false>(dz, a.ldz, x, a.ldx, static_cast<T *>(a.gW), a.ldgw, b / kt * TS, a.N, b % kt * TS, a.K, a.M, sa, sb);
+    piece<T, false>(dz, dz2, a.ldz, x, a.ldx, static_cast<T *>(a.gW), a.ldgw, b / kt * TS, a.N, b % kt * TS, a.K, a.M, sa, sb);
     return;
   }
   b -= a.nw;
@@ -188,10 +195,10 @@ template e2f_status gemm_small<float>(const Gemm &, cudaStream_t);
 template e2f_status gemm_small<__nv_bfloat16>(const Gemm &, cudaStream_t);
 
 template <typename T>
-e2f_status small_grads(const e2f_linear &p, const void *dz, long long ldz, void *gx, long long ldgx, void *gW, long long ldgw,
-                       const void *cp, int ctype, long long cld, int crows, float *gb, bool after, cudaStream_t s) {
+e2f_status small_grads(const e2f_linear &p, const void *dz, const void *dz2, long long ldz, void *gx, long long ldgx, void *gW,
+                       long long ldgw, const void *cp, int ctype, long long cld, int crows, float *gb, bool after, cudaStream_t s) {
   small::Args a{};
-  a.dz = dz; a.ldz = ldz; a.x = p.x; a.ldx = p.ldx; a.W = p.W; a.ldw = p.ldw;
+  a.dz = dz; a.dz2 = dz2; a.ldz = ldz; a.x = p.x; a.ldx = p.ldx; a.W = p.W; a.ldw = p.ldw;
   a.gx = gx; a.ldgx = ldgx; a.gW = gW; a.ldgw = ldgw;
   a.M = (int)p.M; a.N = p.N; a.K = p.K;
   const int kt = (p.K + 31) / 32;
@@ -204,10 +211,11 @@ e2f_status small_grads(const e2f_linear &p, const void *dz, long long ldz, void 
   else E2F_LAUNCH(small::small_grads_kernel<T>, grid, small::NT, 0, s, a);
   return E2F_OK;
 }
-template e2f_status small_grads<float>(const e2f_linear &, const void *, long long, void *, long long, void *, long long,
-                                       const void *, int, long long, int, float *, bool, cudaStream_t);
-template e2f_status small_grads<__nv_bfloat16>(const e2f_linear &, const void *, long long, void *, long long, void *,
-                                               long long, const void *, int, long long, int, float *, bool, cudaStream_t);
+template e2f_status small_grads<float>(const e2f_linear &, const void *, const void *, long long, void *, long long, void *,
+                                       long long, const void *, int, long long, int, float *, bool, cudaStream_t);
+template e2f_status small_grads<__nv_bfloat16>(const e2f_linear &, const void *, const void *, long long, void *, long long,
+                                               void *, long long, const void *, int, long long, int, float *, bool,
+                                               cudaStream_t);
 
 }  // namespace lin
 }  // namespace e2f

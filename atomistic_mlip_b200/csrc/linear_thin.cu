@@ -39,6 +39,24 @@ template <int CPL> __device__ __forceinline__ void store_out(const Epi &e, size_
   }
 }
 
+// ... of dz in two bf16 terms, where it has them.
+template <int CPL> __device__ __forceinline__ void store_dz(const Epi &e, size_t i, const float (&v)[CPL]) {
+  if (!e.out2) {
+    store_out<CPL>(e, i, v);
+    return;
+  }
+  __nv_bfloat16 *h = static_cast<__nv_bfloat16 *>(e.out) + i, *l = static_cast<__nv_bfloat16 *>(e.out2) + i;
+  if constexpr (CPL == 1) {
+    two_terms(v[0], *h, *l);
+  } else {
+    uint2 a, b;
+    two_terms({v[0], v[1]}, a.x, b.x);
+    two_terms({v[2], v[3]}, a.y, b.y);
+    *reinterpret_cast<uint2 *>(h) = a;
+    *reinterpret_cast<uint2 *>(l) = b;
+  }
+}
+
 // KP: inputs, rounded up; CPL: columns a lane; EXTRA: a residual or dL/dout is read.
 template <typename T, int KP, int CPL, bool EXTRA>
 __global__ void __launch_bounds__(NT) thin_kernel(const __grid_constant__ Gemm g) {
@@ -122,7 +140,12 @@ __global__ void __launch_bounds__(NT) thin_kernel(const __grid_constant__ Gemm g
             if (EXTRA) v[c] += y[u][c];
           }
         }
-        if (e.out) store_out<CPL>(e, (size_t)((long long)(m0 + r) * e.ldo) + n, v);
+        const size_t at = (size_t)((long long)(m0 + r) * e.ldo) + n;
+        if (EXTRA && e.mode == MODE_DZ) {
+          if (e.out) store_dz<CPL>(e, at, v);
+        } else {
+          store_out<CPL>(e, at, v);
+        }
       }
     }
   }

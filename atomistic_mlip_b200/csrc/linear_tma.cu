@@ -15,6 +15,9 @@
 // blocks and the epilogue warps add the pieces in registers, rounded to
 // nearest.
 //
+// A may come in two terms (NA = 2: dz of the backward): a stage holds a slice of
+// both, B's is loaded once and multiplied with each.
+//
 // Measured: 8,192 x 4,096 -> 4,096 with GELU and an fp32 residual and result 217 us
 // (1,270 TFLOP/s; without any of them 174, the tensor core's limit); 100,002 x 128 ->
 // 512 SiLU 38 us (3.4 TB/s; without activation 25), where the epilogue's
@@ -46,7 +49,7 @@ template <int EW> constexpr int threads() { return (4 + EW) * 32; }
 template <int EW> constexpr int staging() { return EW * 32 * 32 * 4; }
 template <int EW> constexpr int sbias() { return EW * 32 * 4; }
 template <int EW> constexpr int ring() { return EW == 16 ? 147456 : 196608; }
-template <int BN> constexpr int stage_bytes() { return (BM + BN) * BK * 2; }
+template <int BN, int NA> constexpr int stage_bytes() { return (NA * BM + BN) * BK * 2; }
 template <int EW> constexpr size_t smem_bytes() { return ring<EW>() + staging<EW>() + sbias<EW>() + 256 + 1024; }
 
 struct Args {
@@ -90,7 +93,9 @@ template <bool MN> __device__ __forceinline__ uint64_t slice_desc(uint32_t saddr
 // it, and TMA takes that out.  Against turning the chunk through shared memory
 // this halves the LSU wavefronts, which bound short contractions (100,002 x 128 ->
 // 512: 80 % of their peak): per chunk 32 for the accumulators, 16 in, 16 out, 8
-// for the bias.  Rows of 64 bytes, 64-byte swizzle.
+// for the bias.  Rows of 64 bytes, 64-byte swizzle.  Of a warp's three buffers the residual's chunks
+// take turns in all (two loads ahead); dz, which leaves in two terms, has its second
+// one in the last and dL/dout in the others, one load ahead.
 constexpr int IO_BUF = 2048;
 template <int EPI, int BN> constexpr int io_bufs() { return EPI >= RES ? 3 : BN / 128; }   // (a chunk or two of a tile)
 template <int EPI, int BN> constexpr int io_ring() { return EPI >= RES ? 126976 : BN == 256 ? 147456 : 180224; }
@@ -127,12 +132,13 @@ __device__ __forceinline__ float transposed_sum(float (&v)[32], int lane) {
 }
 
 template <int BN, int EPI>
-__device__ __forceinline__ bool io_epilogue(const Args &a, const CUtensorMap *to, const CUtensorMap *tx, uint8_t *bufs,
-                                            float *sbiases, uint64_t *xbars, uint64_t *tfull, uint64_t *tempty,
+__device__ __forceinline__ bool io_epilogue(const Args &a, const CUtensorMap *to, const CUtensorMap *to2,
+                                            const CUtensorMap *tx, uint8_t *bufs, float *sbiases, uint64_t *xbars, uint64_t *tfull, uint64_t *tempty,
                                             uint32_t tmem, int ew, int lane) {
   using namespace tc;
   constexpr uint32_t LIMIT = 1u << 26;
   constexpr int BW = BN / 4, NCH = BW / 32, NB = io_bufs<EPI, BN>();
+  constexpr int NX = EPI == DZ ? NB - 1 : NB;   // buffers that the chunks take in turn
   constexpr bool EXTRA = EPI >= RES;
   const Epi &e = a.g.e;
   const int quarter = ew & 3, cols = (ew >> 2) * BW;
@@ -151,7 +157,7 @@ __device__ __forceinline__ bool io_epilogue(const Args &a, const CUtensorMap *to
         mbar_arrive_expect_tx(&xbar[pb], IO_BUF);
         tma_load_2d(buf + pb * IO_BUF, tx, n, m, &xbar[pb]);
         ++pc;
-        if (++pb == NB) pb = 0;
+        if (++pb == NX) pb = 0;
         return;
       }
       pi += gridDim.x;
@@ -161,7 +167,7 @@ __device__ __forceinline__ bool io_epilogue(const Args &a, const CUtensorMap *to
   };
   if (EXTRA && lane == 0) {
     load_next();
-    load_next();
+    if (EPI != DZ) load_next();
   }
   int u = 0, b = 0, bias_of = -1;
   uint32_t xph = 0;
@@ -227,23 +233,47 @@ __device__ __forceinline__ bool io_epilogue(const Args &a, const CUtensorMap *to
             v[8 * j + 2 * k + 1] = r.y;
           }
         }
-        // the buffer of the chunk before has left: the chunk after the next goes there
+        // the chunk before has left its buffers: the chunk after the next (dz: the next)
+        // goes there
         if (lane == 0) {
           stores_read<0>();
           load_next();
         }
+        if (EPI == DZ) __syncwarp();
       } else {
         if (lane == 0) stores_read<NB - 1>();
         __syncwarp();
       }
+      if (EPI == DZ) {
+        uint4 *rest = reinterpret_cast<uint4 *>(buf + NX * IO_BUF + lane * 64);
+        if (e.out) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-        row[j ^ sw] = make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
-                                 pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
-      fence_async_smem();
-      __syncwarp();
-      if (lane == 0 && (EPI != DZ || e.out)) tma_store_2d(to, buf + b * IO_BUF, n, mw);
-      if (++b == NB) { b = 0; xph ^= 1; }
+          for (int j = 0; j < 4; ++j) {
+            uint4 h, l;
+            two_terms({v[8 * j], v[8 * j + 1]}, h.x, l.x);
+            two_terms({v[8 * j + 2], v[8 * j + 3]}, h.y, l.y);
+            two_terms({v[8 * j + 4], v[8 * j + 5]}, h.z, l.z);
+            two_terms({v[8 * j + 6], v[8 * j + 7]}, h.w, l.w);
+            row[j ^ sw] = h;
+            rest[j ^ sw] = l;
+          }
+          fence_async_smem();
+          __syncwarp();
+          if (lane == 0) {
+            tma_store_2d(to, buf + b * IO_BUF, n, mw);
+            tma_store_2d(to2, buf + NX * IO_BUF, n, mw);
+          }
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          row[j ^ sw] = make_uint4(pack_bf16x2(v[8 * j], v[8 * j + 1]), pack_bf16x2(v[8 * j + 2], v[8 * j + 3]),
+                                   pack_bf16x2(v[8 * j + 4], v[8 * j + 5]), pack_bf16x2(v[8 * j + 6], v[8 * j + 7]));
+        fence_async_smem();
+        __syncwarp();
+        if (lane == 0) tma_store_2d(to, buf + b * IO_BUF, n, mw);
+      }
+      if (++b == NX) { b = 0; xph ^= 1; }
       if (EPI == DZ && e.colpart) {
         const float s = transposed_sum(v, lane);
         if (a.s.keep) sum[0] += s;
@@ -273,15 +303,17 @@ __device__ __forceinline__ bool io_epilogue(const Args &a, const CUtensorMap *to
   return ok;
 }
 
-template <bool AMN, bool BMN, int BN, bool LONGK, int EPI, int EW, bool IO>
+// t2: A's second term (NA = 2) or the second term of the results (IO, DZ).
+template <bool AMN, bool BMN, int BN, bool LONGK, int EPI, int EW, bool IO, int NA>
 __global__ void __launch_bounds__(threads<EW>(), 1)
 gemm_tma_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ CUtensorMap tbm,
                 const __grid_constant__ CUtensorMap to, const __grid_constant__ CUtensorMap tx,
-                const __grid_constant__ Args a) {
+                const __grid_constant__ CUtensorMap t2, const __grid_constant__ Args a) {
   using namespace tc;
   constexpr int RING = IO ? io_ring<EPI, BN>() : ring<EW>(), STAGING = IO ? 16 * io_bufs<EPI, BN>() * IO_BUF : staging<EW>(),
                 SBIAS = IO ? IO_SBIAS : sbias<EW>();
-  constexpr int ABYTES = BM * BK * 2, BBYTES = BN * BK * 2;
+  constexpr int ATERM = BM * BK * 2, ABYTES = NA * ATERM, BBYTES = BN * BK * 2;
+  static_assert(RING / (ABYTES + BBYTES) >= 2, "");
   constexpr uint32_t LIMIT = 1u << 26;
   extern __shared__ uint8_t smem_raw[];
   uint8_t *smem = reinterpret_cast<uint8_t *>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~(uintptr_t)1023);
@@ -332,6 +364,7 @@ gemm_tma_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ 
           if (!ok) break;
           mbar_arrive_expect_tx(&full[s], SB);
           load_slice<AMN, BM>(ringp + s * SB, &ta, t.m0, kb * BK, &full[s]);
+          if (NA == 2) load_slice<AMN, BM>(ringp + s * SB + ATERM, &t2, t.m0, kb * BK, &full[s]);
           if (!bres) load_slice<BMN, BN>(ringp + s * SB + ABYTES, &tbm, t.n0, kb * BK, &full[s]);
           if (++s == ST) { s = 0; ph ^= 1; }
         }
@@ -360,8 +393,10 @@ gemm_tma_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ 
             tc_fence_after();
             const uint32_t a0 = smem_addr(ringp + s * SB), b0 = bres ? smem_addr(smem + kb * BBYTES) : a0 + ABYTES;
 #pragma unroll
-            for (int k = 0; k < BK; k += 16)
+            for (int k = 0; k < BK; k += 16) {
               mma_bf16_ss(acc, slice_desc<AMN>(a0, k), slice_desc<BMN>(b0, k), id, kb > kc || k > 0 ? 1u : 0u);
+              if (NA == 2) mma_bf16_ss(acc, slice_desc<AMN>(a0 + ATERM, k), slice_desc<BMN>(b0, k), id, 1u);
+            }
             mma_commit(&empty[s]);
             if (++s == ST) { s = 0; ph ^= 1; }
           }
@@ -371,7 +406,7 @@ gemm_tma_kernel(const __grid_constant__ CUtensorMap ta, const __grid_constant__ 
       if (!ok) atomicExch(a.err, E2F_ERR_TIMEOUT);
     }
   } else if (IO && warp >= 4) {
-    const bool ok = io_epilogue<BN, EPI>(a, &to, &tx, smem + RING, reinterpret_cast<float *>(smem + RING + STAGING), xbar,
+    const bool ok = io_epilogue<BN, EPI>(a, &to, &t2, &tx, smem + RING, reinterpret_cast<float *>(smem + RING + STAGING), xbar,
                                          tfull, tempty, tmem, warp - 4, lane);
     if (!ok && lane == 0) atomicExch(a.err, E2F_ERR_TIMEOUT);
   } else if (!IO && warp >= 4) {
@@ -537,57 +572,60 @@ static bool encode(CUtensorMap *m, const void *p, long long rows, long long cols
             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <bool AMN, bool BMN, int BN, bool LONGK, int EPI, int EW, bool IO>
-static e2f_status launch_epi(const CUtensorMap &ta, const CUtensorMap &tb, Args a, cudaStream_t s) {
+template <bool AMN, bool BMN, int BN, bool LONGK, int EPI, int EW, bool IO, int NA>
+static e2f_status launch_epi(const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorMap &ta2, Args a, cudaStream_t s) {
   // B stays in shared memory for the launch where every CTA has one column tile
   // and five stages of A fit beside it (with three, too few bytes in flight:
   // 100,002 x 512 -> 128 33 us, 30 with B in the ring).
   constexpr int RING = IO ? io_ring<EPI, BN>() : ring<EW>();
-  const long long bres = (long long)a.s.nkb * BN * BK * 2, abytes = BM * BK * 2;
+  const long long bres = (long long)a.s.nkb * BN * BK * 2, abytes = NA * BM * BK * 2;
   a.bres = EW == 16 && a.s.fixed && a.g.kper == a.s.nkb && bres + 5 * abytes <= RING ? (int)bres : 0;
-  a.st = std::min<int>(MAX_ST, (RING - a.bres) / (a.bres ? (int)abytes : stage_bytes<BN>()));
-  CUtensorMap to{}, tx{};
+  a.st = std::min<int>(MAX_ST, (RING - a.bres) / (a.bres ? (int)abytes : stage_bytes<BN, NA>()));
+  CUtensorMap to{}, tx{}, t2 = ta2;
   if (IO) {
     const Epi &e = a.g.e;
     if ((e.out && !encode(&to, e.out, a.g.M, a.g.N, e.ldo, 32, 32)) ||
+        (EPI == DZ && e.out2 && !encode(&t2, e.out2, a.g.M, a.g.N, e.ldo, 32, 32)) ||
         (EPI >= RES && !encode(&tx, e.extra, a.g.M, a.g.N, e.lde, 32, 32))) {
       set_cuda_error(cudaErrorInvalidValue, "cuTensorMapEncodeTiled");
       return E2F_ERR_CUDA;
     }
   }
-  constexpr auto k = gemm_tma_kernel<AMN, BMN, BN, LONGK, EPI, EW, IO>;
+  constexpr auto k = gemm_tma_kernel<AMN, BMN, BN, LONGK, EPI, EW, IO, NA>;
   constexpr size_t smem = IO ? io_smem<EPI, BN>() : smem_bytes<EW>();
   E2F_CUDA_TRY(allow_smem<k>(smem, LONGK ? 168 : 0));
-  E2F_LIN_LAUNCH(a.g, k, a.grid, threads<EW>(), smem, s, ta, tb, to, tx, a);
+  E2F_LIN_LAUNCH(a.g, k, a.grid, threads<EW>(), smem, s, ta, tb, to, tx, t2, a);
   return E2F_OK;
 }
 
-template <bool AMN, bool BMN, int BN, bool LONGK, int EPI>
-static e2f_status launch_kind(const CUtensorMap &ta, const CUtensorMap &tb, const Args &a, cudaStream_t s) {
+template <bool AMN, bool BMN, int BN, bool LONGK, int EPI, int NA>
+static e2f_status launch_kind(const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorMap &ta2, const Args &a, cudaStream_t s) {
   if constexpr (!LONGK) {
     const Epi &e = a.g.e;
     if (a.g.kper <= short_k(EPI)) {
       // (a dz that is not stored takes the same kernel: its column sums have one order)
       const bool io = e.mode != MODE_PART && e.otype == E2F_BF16 && (e.out ? tma_operand(e.out, e.ldo) : EPI == DZ) &&
                       (EPI < RES || (e.etype == E2F_BF16 && tma_operand(e.extra, e.lde)));
-      if (io) return launch_epi<AMN, BMN, BN, false, EPI, 16, true>(ta, tb, a, s);
-      return launch_epi<AMN, BMN, BN, false, EPI, 16, false>(ta, tb, a, s);
+      if (io) return launch_epi<AMN, BMN, BN, false, EPI, 16, true, NA>(ta, tb, ta2, a, s);
+      return launch_epi<AMN, BMN, BN, false, EPI, 16, false, NA>(ta, tb, ta2, a, s);
     }
   }
-  return launch_epi<AMN, BMN, BN, LONGK, EPI, 8, false>(ta, tb, a, s);
+  return launch_epi<AMN, BMN, BN, LONGK, EPI, 8, false, NA>(ta, tb, ta2, a, s);
 }
 
 template <bool AMN, bool BMN, int BN, bool LONGK>
-static e2f_status launch(const CUtensorMap &ta, const CUtensorMap &tb, const Args &a, cudaStream_t s) {
+static e2f_status launch(const CUtensorMap &ta, const CUtensorMap &tb, const CUtensorMap &ta2, const Args &a, cudaStream_t s) {
   if constexpr (!AMN && !BMN) {
     switch (epi_kind(a.g.e)) {
-      case DZ: return launch_kind<AMN, BMN, BN, LONGK, DZ>(ta, tb, a, s);
-      case RES: return launch_kind<AMN, BMN, BN, LONGK, RES>(ta, tb, a, s);
-      case ACT: return launch_kind<AMN, BMN, BN, LONGK, ACT>(ta, tb, a, s);
+      case DZ: return launch_kind<AMN, BMN, BN, LONGK, DZ, 1>(ta, tb, ta2, a, s);
+      case RES: return launch_kind<AMN, BMN, BN, LONGK, RES, 1>(ta, tb, ta2, a, s);
+      case ACT: return launch_kind<AMN, BMN, BN, LONGK, ACT, 1>(ta, tb, ta2, a, s);
       default: break;
     }
   }
-  return launch_kind<AMN, BMN, BN, LONGK, PLAIN>(ta, tb, a, s);
+  if constexpr (BMN)   // the products of dz
+    if (a.g.A2) return launch_kind<AMN, BMN, BN, LONGK, PLAIN, 2>(ta, tb, ta2, a, s);
+  return launch_kind<AMN, BMN, BN, LONGK, PLAIN, 1>(ta, tb, ta2, a, s);
 }
 
 }  // namespace tma
@@ -615,8 +653,11 @@ e2f_status gemm_tma(const Gemm &g, int splits, int bn, int sms, cudaStream_t s, 
       if (rows_out) *rows_out = even / a.s.nt * 4;
     }
   }
-  CUtensorMap ta, tb;
-  const bool ok = (AMN ? encode(&ta, g.A, g.K, g.M, g.lda, 64) : encode(&ta, g.A, g.M, g.K, g.lda, BM)) &&
+  CUtensorMap ta, tb, ta2{};
+  auto encode_a = [&](CUtensorMap *m, const void *p) {
+    return AMN ? encode(m, p, g.K, g.M, g.lda, 64) : encode(m, p, g.M, g.K, g.lda, BM);
+  };
+  const bool ok = encode_a(&ta, g.A) && (!g.A2 || encode_a(&ta2, g.A2)) &&
                   (BMN ? encode(&tb, g.B, g.K, g.N, g.ldb, 64) : encode(&tb, g.B, g.N, g.K, g.ldb, bn));
   if (!ok) {
     set_cuda_error(cudaErrorInvalidValue, "cuTensorMapEncodeTiled");
@@ -624,8 +665,8 @@ e2f_status gemm_tma(const Gemm &g, int splits, int bn, int sms, cudaStream_t s, 
   }
   const bool longk = long_chain(g);
   if (bn == 256)
-    return longk ? launch<AMN, BMN, 256, true>(ta, tb, a, s) : launch<AMN, BMN, 256, false>(ta, tb, a, s);
-  return longk ? launch<AMN, BMN, 128, true>(ta, tb, a, s) : launch<AMN, BMN, 128, false>(ta, tb, a, s);
+    return longk ? launch<AMN, BMN, 256, true>(ta, tb, ta2, a, s) : launch<AMN, BMN, 256, false>(ta, tb, ta2, a, s);
+  return longk ? launch<AMN, BMN, 128, true>(ta, tb, ta2, a, s) : launch<AMN, BMN, 128, false>(ta, tb, ta2, a, s);
 }
 template e2f_status gemm_tma<false, false>(const Gemm &, int, int, int, cudaStream_t, int *);
 template e2f_status gemm_tma<false, true>(const Gemm &, int, int, int, cudaStream_t, int *);

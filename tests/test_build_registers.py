@@ -27,5 +27,5 @@ def test_too_few_registers_end_the_build():
 def test_the_names_are_those_of_the_sources():
     src = {n: open(f"{build_mod.CSRC}/{n}.cu").read() for n in ("linear_reg", "linear_tma")}
     assert "gemm_reg_kernel(" in src["linear_reg"] and "LAUNCH_REGS = 72" in src["linear_reg"]
-    assert "template <bool AMN, bool BMN, int BN, bool LONGK, int EPI, int EW, bool IO>" in src["linear_tma"]
+    assert "template <bool AMN, bool BMN, int BN, bool LONGK, int EPI, int EW, bool IO" in src["linear_tma"]
     assert "gemm_tma_kernel(" in src["linear_tma"] and "LONGK ? 168 : 0" in src["linear_tma"]

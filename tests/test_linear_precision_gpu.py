@@ -1,5 +1,6 @@
 """What the linear layers' kernels do for their precision, each at a size where its
-loss would show: three terms of an fp32 operand, and chains of MMAs that end.
+loss would show: three terms of an fp32 operand, chains of MMAs that end, two terms
+of dz in the bf16 backward.
 
 Three terms: an fp32 value times one, plus zeros, is itself.
 Chains: the tensor core's accumulation truncates, by measurement about 1e-8 of the
@@ -9,7 +10,7 @@ K / 1,024 pieces are added with a rounding each (2^-24).  One chain over 16,384
 products would be off by 1e-5, five times the bound."""
 import pytest
 
-from .test_linear_gpu import _check_backward, _check_forward, _make
+from .test_linear_gpu import E24, EB, SHAPES, _acc, _act, _check_backward, _check_forward, _fwd_ref, _make
 
 pytestmark = pytest.mark.gpu
 
@@ -98,4 +99,58 @@ def test_split_contractions_of_tall_products(cuda_ok, M, C, N, dt):
     e2f.linear_forward(x, W, bias=b, residual=out, out=out, act="gelu")
     _check_forward(out, x, W, b, r, "gelu")
     _check_backward(*e2f.linear_backward(x, W, r, bias=b, act="silu"), x, W, b, r, "silu")
+    assert e2f.stream_status() == 0
+
+
+@pytest.mark.parametrize("M,K,N,Q", [s for s in SHAPES if s[0]] + [(3000, 128, 514, 1), (900, 77, 130, 1), (10304, 128, 512, 1),
+                                                                   (3001, 8, 100, 1), (2, 300, 70, 1), (4099, 1000, 2050, 1)])
+@pytest.mark.parametrize("gt,act", [("bfloat16", "silu"), ("float32", "gelu"), ("float32", "none"), ("bfloat16", "none")])
+def test_bf16_gradients_are_rounded_once(cuda_ok, M, K, N, Q, gt, act):
+    """dz enters the products of bf16 layers in two bf16 terms: each bf16 result is off
+    by its own rounding, 2^-16 of dz (2^-8 of what the first term leaves, which is at
+    most 2^-8 where it is rounded; 2^-16 where it is cut) and what the fp32 sums of
+    twice as many products lose.  One term would add 2^-8 of dz."""
+    import torch
+    from atomistic_mlip_b200 import e2f
+    x, W, b, g = _make(M, K, N, Q, torch.bfloat16, 7 * M + K + N)
+    dy = torch.randn(M, N, generator=g, device="cuda").to(getattr(torch, gt))
+    gx, gw, _ = e2f.linear_backward(x, W, dy, bias=b, act=act)
+    assert e2f.stream_status() == 0
+    z, S = _fwd_ref(x, W, b, act)
+    _, d = _act(z, act)
+    dz = dy.double() * d
+    edz = dy.double().abs() * (0.8 * _acc(K) * S + 16 * E24 * (1 + z.abs())) if act != "none" else dz.abs() * 0
+    edz = edz + 1.01 * 2.0 ** -16 * (dz.abs() + edz)
+    mag = dz.abs() + edz
+    for got, a, e, m, o in ((gx, dz, edz, mag, W.double()), (gw, dz.t(), edz.t(), mag.t(), x.double())):
+        r = a @ o
+        t = e @ o.abs() + _acc(2 * a.shape[1]) * (m @ o.abs())
+        assert bool(((got.double() - r).abs() <= t + (EB + E24) * 1.01 * (r.abs() + t)).all())
+
+
+@pytest.mark.parametrize("M,K,N", [(300, 72, 96), (900, 77, 130), (3000, 128, 512), (2000, 600, 520)])
+def test_bf16_gradients_beside_infinities(cuda_ok, M, K, N):
+    """An infinity of dL/dout, W or x meets both terms of dz as it meets dz."""
+    import torch
+    from atomistic_mlip_b200 import e2f
+    inf, nan = float("inf"), float("nan")
+    x, W, _, g = _make(M, K, N, 1, torch.bfloat16, M)
+    x = x.contiguous()
+    dy = torch.randn(M, N, generator=g, device="cuda")
+    dy[::2] = dy[::2].bfloat16().float()             # nothing left for the second term
+    dy[0] = 0.0
+    x[2, 3], x[3, 5], W[4, 6], W[7, 8] = inf, -inf, -inf, nan
+    for planted in (False, True):
+        if planted:
+            dy[5, 2], dy[6, 9], dy[11, 11] = inf, -inf, torch.finfo(torch.float32).max
+        gx, gw, _ = e2f.linear_backward(x, W, dy)
+        d8, x8, W8 = dy.double(), x.double(), W.double()
+        if planted:                                  # (bf16 results: FLT_MAX itself is one step above their largest)
+            d8 = d8.clone()
+            d8[11, 11] = float(torch.finfo(torch.bfloat16).max)
+        for got, ref in ((gx, d8 @ W8), (gw, d8.t() @ x8)):
+            assert torch.equal(torch.isnan(got), torch.isnan(ref))
+            for s in (inf, -inf):
+                near = (ref == s) | (ref * (1 if s > 0 else -1) > 3e38)
+                assert bool((got == s)[ref == s].all()) and not bool(((got == s) & ~near).any())
     assert e2f.stream_status() == 0
