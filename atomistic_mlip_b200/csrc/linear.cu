@@ -247,7 +247,7 @@ static e2f_status run_gemm(Gemm g, cudaStream_t s, int *rows_out = nullptr) {
 
 // bf16 x and W on 16-byte rows for large products, which then go by TMA: there the
 // copies cost less than element-wise loads in the product (100,001 x 127 -> 129
-// with its gradient 239 us, 170 us so; below 2^29 multiply-adds it is the other
+// with its gradient 239 us, 170 us so, dz in one term; below 2^29 multiply-adds it is the other
 // way round).  fp32 operands pass through registers either way.  q: p with the
 // copies in place of what was unaligned; after: whether a kernel was launched.
 template <typename T>

@@ -11,8 +11,8 @@
 // operands costs the tensor core 24 MMAs of 64 cycles and shared memory 96 KB
 // written and 192 KB read (2,304 cycles): shared memory bounds it, at 265
 // TFLOP/s nominal.
-// Measured (fp32): 4,096 x 4,096 -> 2,048 408 us, 168 TFLOP/s; 100,002 x 128 -> 512
-// 147 us a call; 10,304 x 128 -> 128 10 us, all of it latency.
+// Measured (fp32): 4,096 x 4,096 -> 2,048 410 us, 168 TFLOP/s; 100,002 x 128 -> 512
+// 125 us, with SiLU 140; 10,304 x 128 -> 128 10 us, all of it latency.
 #include <algorithm>
 
 #include "linear_epi.cuh"

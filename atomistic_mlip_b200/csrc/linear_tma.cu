@@ -39,7 +39,7 @@ namespace tma {
 
 constexpr int BM = 128, BK = 64;
 // Contractions of up to so many blocks of 64 get 16 epilogue warps: there the
-// epilogue is the longer part of a tile (4,099 x 1,000 -> 2,050, dz: 45 us
+// epilogue is the longer part of a tile (4,099 x 1,000 -> 2,050, dz in one term: 45 us
 // against 63; 65,536 x 768 -> 1,024 without an extra operand: 97 against 94).
 constexpr int short_k(int epi) { return epi >= RES ? 16 : 8; }
 
