@@ -70,8 +70,8 @@ __device__ __forceinline__ void product(float (&acc)[2][2], const T *A, const T 
   }
 }
 template <typename T, bool A_CONTIG>
-__device__ __forceinline__ void piece(const T *A, const T *A2, long long lda, const T *B, long long ldb, T *out, long long ldo, int r0,
-                                      int rn, int c0, int cn, int kn, float (*sa)[PITCH], float (*sb)[PITCH]) {
+__device__ __forceinline__ void piece(const T *A, const T *A2, long long lda, const T *B, long long ldb, T *out,
+                                      long long ldo, int r0, int rn, int c0, int cn, int kn, float (*sa)[PITCH], float (*sb)[PITCH]) {
   float acc[2][2];
   product<T, A_CONTIG, false>(acc, A, A2, lda, B, ldb, r0, rn, c0, cn, kn, sa, sb);
 #pragma unroll
@@ -134,7 +134,8 @@ struct Args {
 template <typename T> __global__ void __launch_bounds__(NT) small_grads_kernel(const __grid_constant__ Args a) {
   __shared__ float sa[TS][PITCH], sb[TS][PITCH];
   after_previous();
-  const T *dz = static_cast<const T *>(a.dz), *dz2 = static_cast<const T *>(a.dz2), *x = static_cast<const T *>(a.x), *W = static_cast<const T *>(a.W);
+  const T *dz = static_cast<const T *>(a.dz), *dz2 = static_cast<const T *>(a.dz2);
+  const T *x = static_cast<const T *>(a.x), *W = static_cast<const T *>(a.W);
   const int kt = (a.K + TS - 1) / TS;
   int b = blockIdx.x;
   if (b < a.nx) {

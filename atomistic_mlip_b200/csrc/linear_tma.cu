@@ -133,8 +133,8 @@ __device__ __forceinline__ float transposed_sum(float (&v)[32], int lane) {
 
 template <int BN, int EPI>
 __device__ __forceinline__ bool io_epilogue(const Args &a, const CUtensorMap *to, const CUtensorMap *to2,
-                                            const CUtensorMap *tx, uint8_t *bufs, float *sbiases, uint64_t *xbars, uint64_t *tfull, uint64_t *tempty,
-                                            uint32_t tmem, int ew, int lane) {
+                                            const CUtensorMap *tx, uint8_t *bufs, float *sbiases, uint64_t *xbars,
+                                            uint64_t *tfull, uint64_t *tempty, uint32_t tmem, int ew, int lane) {
   using namespace tc;
   constexpr uint32_t LIMIT = 1u << 26;
   constexpr int BW = BN / 4, NCH = BW / 32, NB = io_bufs<EPI, BN>();

@@ -414,7 +414,8 @@ E2F_API e2f_status e2f_linear_forward(const e2f_linear *p, const void *residual,
  * E2F_BF16 dz enters the products as two bf16 terms, 16 bits of it, so that
  * grad_x and grad_W are as exact as their own rounding.  All outputs
  * are fully overwritten (M = 0: grad_W and grad_bias are zeros) and repeat
- * bit for bit, whichever of them are asked for.  No output may overlap an input or another output.  A row of
+ * bit for bit, whichever of them are asked for.  No output may overlap an input
+ * or another output.  A row of
  * zeros in grad_out adds nothing as long as its row of x is finite (0 * inf is
  * NaN here too).  Fully asynchronous.
  */
